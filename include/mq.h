@@ -56,7 +56,7 @@ typedef enum mq_status {
   MQ_OK = 0,
   MQ_ERR_NULL = 1,      /* a required pointer is NULL                          */
   MQ_ERR_SHAPE = 2,     /* a size is out of range (see each entry point)       */
-  MQ_ERR_PRECISION = 3, /* r is not 2, 3, 4, 6 or 8 */
+  MQ_ERR_PRECISION = 3, /* r is not 2, 3, 4, 6 or 8; an unknown type or format */
   MQ_ERR_GROUP = 4,     /* group is neither K nor 128                          */
   MQ_ERR_ALIGN = 5,     /* a pointer is not 16-byte aligned                    */
   MQ_ERR_WORKSPACE = 6, /* workspace missing or smaller than required          */
@@ -386,6 +386,171 @@ MQ_API size_t mq_mlp_workspace_bytes(int64_t M, int64_t F);
 MQ_API mq_status mq_mlp_decode(const mq_linear* up, const mq_linear* gate, const mq_linear* down, int r,
                         int act, const uint16_t* x, int64_t M, float* y, void* workspace,
                         size_t workspace_bytes, void* stream);
+
+
+/*
+ * Attention over an 8-bit key/value cache.
+ *
+ * The cache.  Keys and values are held in pages of `block` tokens, as 8-bit
+ * codes with ONE fp32 scale per page and key/value head for each of the two:
+ * value = code * scale.  A page of a head is one contiguous block of
+ * block * dim bytes:
+ *   k        uint8 [pages, heads, block, dim]
+ *   v        uint8 [pages, heads, dim, block]   (dim-major: the products of
+ *            the attention contract over tokens, so a lane's operand is 16
+ *            consecutive bytes in both arrays)
+ *   k_scale, v_scale  fp32 [pages, heads]
+ * format: MQ_KV_INT8 (two's complement, -127..127) or MQ_KV_E4M3 (8-bit
+ * floating point, 4 exponent and 3 mantissa bits, largest value 448).
+ * Sizes: 1 <= pages < 2^31, 1 <= heads <= 4096, block in {16, 32, 64, 128},
+ * dim in {64, 128, 256}; k and v 16-byte aligned, the scales 4-byte.  The
+ * arrays may exceed 4 GiB.
+ */
+enum { MQ_KV_INT8 = 0, MQ_KV_E4M3 = 1 };
+typedef struct mq_kv_cache {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages;
+  int32_t heads, block, dim, format;
+} mq_kv_cache;
+
+/*
+ * Which tokens a call is about.  `rows` token rows (of q, k, v, outputs)
+ * belong to `seqs` sequences: sequence s owns rows q_start[s] ..
+ * q_start[s+1] - 1, its last n = q_start[s+1] - q_start[s] tokens, at the
+ * positions kv_len[s] - n .. kv_len[s] - 1 (kv_len counts the tokens cached,
+ * these n among them).  Position p of sequence s is held in page
+ * page_table[s, p / block] at place p % block.
+ *   q_start     int32 [seqs + 1], increasing from 0, at most `rows`
+ *   kv_len      int32 [seqs]
+ *   page_table  int32 [seqs, table_pages]
+ *   max_new     an upper bound of every n (sizes the launch)
+ * The three arrays live on the DEVICE and are read when the work runs, so a
+ * captured graph follows what they hold at each replay.  n = 0 (an idle slot)
+ * and kv_len = 0 are fine.  Rows at and beyond q_start[seqs] are neither read
+ * nor written.  What the host cannot check is bounded on the device: a page
+ * index outside [0, pages) and positions below 0 or beyond table_pages *
+ * block hold no token (nothing is written there, and attention sees no key),
+ * rows beyond `rows` and tokens beyond max_new are not touched.
+ * Sizes: 0 <= rows < 2^31, 1 <= seqs <= 65535, 1 <= table_pages,
+ * table_pages * block < 2^31, 1 <= max_new <= 2^24; pointers 4-byte aligned.
+ */
+typedef struct mq_kv_batch {
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int64_t rows;
+  int32_t seqs, table_pages, max_new;
+} mq_kv_batch;
+
+/*
+ * Rotary positions: pair i (0 <= i < rot / 2) of a head turns by the angle
+ * a = position * freq[i] (formed, reduced and turned in float64, so far
+ * positions keep their angles):
+ *   (x1, x2) -> factor * (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
+ * rounded once to fp32 and from there to bf16 (nearest even).
+ *   freq         float64 [rot / 2] on the device, 8-byte aligned
+ *   rot          entries of a head that turn, a multiple of 8, 8 <= rot <= dim;
+ *                the others pass through (rounded to bf16)
+ *   interleaved  0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1)
+ *   factor       1 unless the frequencies' scaling asks for another
+ */
+typedef struct mq_rope_spec {
+  const double* freq;
+  double factor;
+  int32_t rot, interleaved;
+} mq_rope_spec;
+
+/* Element type of an activation argument. */
+enum { MQ_BF16 = 0, MQ_F32 = 1 };
+
+/*
+ * mq_rope: rotate x at explicit positions.
+ *   x          bf16 or fp32 (x_type) [rows, heads, dim]; a row of heads * dim
+ *              consecutive entries starts every x_stride entries (so x may be
+ *              a part of fused projection rows)
+ *   positions  int32 [rows] on the device
+ *   out        bf16 bits [rows, heads, dim], rows every out_stride entries
+ * x and out 16-byte aligned, strides multiples of 8 and >= heads * dim.
+ * out may be x itself (same address, bf16, same stride); otherwise they must
+ * not overlap.  Sizes: rows >= 0 (0 enqueues nothing), heads >= 1,
+ * 8 <= dim <= 1024, dim % 8 == 0, heads * dim <= 2^20, rows <= 2^24.
+ */
+MQ_API mq_status mq_rope(const mq_rope_spec* rope, const int32_t* positions, const void* x,
+                  int x_type, int64_t x_stride, int64_t rows, int64_t heads, int64_t dim,
+                  uint16_t* out, int64_t out_stride, void* stream);
+
+/*
+ * mq_cache_append: quantize the batch's rows of k and v into the cache at
+ * their positions; with `rope`, k is turned by its position first; with q, the
+ * queries are turned too (or only rounded to bf16, without `rope`) and written
+ * to q_out, in the same launch.
+ * Values are bf16(k), bf16(v) (after the rotation).  For each page and head
+ * that gets tokens, amax = the largest magnitude among its new finite values,
+ *   fresh = amax * fl32(1/Q) in fp32, Q = 127 (int8) or 448 (e4m3); 0 if
+ *           below 2^-100;
+ *   scale = fresh, or max(old scale, fresh) if the page holds earlier tokens
+ *           of the sequence, whose codes c become round(c * old / scale) when
+ *           the scale grows;
+ *   code = round(value / scale), the exact quotient to the nearest code, ties
+ *          to even; all codes 0 if scale is 0.
+ * Infinities become the largest code of their sign, NaN becomes 0, so a cache
+ * written by this call holds numbers only.  Places of a page beyond the
+ * sequence keep their bytes.
+ *   k, v   bf16 or fp32 (x_type) [rows, heads, dim], rows every kv_stride
+ *   q      same type [rows, q_heads, dim], rows every q_stride; or NULL
+ *   q_out  bf16 bits [rows, q_heads, dim] contiguous; NULL exactly if q is
+ * Alignment as mq_rope (strides multiples of 8; 16-byte pointers).  No two
+ * sequences of one call may write the same page (a page shared for reading,
+ * such as a common prefix, is fine if it is full); if they do, that page's
+ * contents are unspecified.  1 <= q_heads, q_heads * dim <= 2^20.
+ */
+MQ_API mq_status mq_cache_append(const mq_kv_cache* cache, const mq_kv_batch* batch,
+                          const mq_rope_spec* rope, const void* k, const void* v,
+                          int64_t kv_stride, const void* q, int64_t q_stride, int64_t q_heads,
+                          int x_type, uint16_t* q_out, void* stream);
+
+/*
+ * mq_cache_read: the batch's tokens back from the cache, code * scale rounded
+ * to fp32 and, for MQ_BF16, from there to bf16:
+ *   k_out, v_out  out_type [rows, heads, dim] contiguous, 16-byte aligned;
+ *                 either may be NULL (not both).
+ * Rows whose position holds no token (see mq_kv_batch) become 0.
+ */
+MQ_API mq_status mq_cache_read(const mq_kv_cache* cache, const mq_kv_batch* batch, void* k_out,
+                        void* v_out, int out_type, void* stream);
+
+/*
+ * mq_cache_attend: attention of the batch's query rows over their sequences'
+ * cached tokens, q_heads = group * heads query heads, head h reading
+ * key/value head h / group.  For the query at position p:
+ *   t_j = scale * <q, k_j>,  t_j = softcap * tanh(t_j / softcap) if softcap > 0,
+ *   out = sum_j softmax(t)_j v_j  (bf16),   lse = log sum_j exp t_j  (fp32)
+ * over the positions j < kv_len, with causal j <= p, and with window > 0
+ * j > p - window.  A query that sees no key gets out = 0 and lse = -inf.
+ * Scores, their maximum and their sum are fp32; the probabilities enter the
+ * second product in 11 bits (fp16, scaled to their row's maximum).
+ *   q    bf16 bits [rows, q_heads, dim], rows every q_stride entries
+ *   out  bf16 bits [rows, q_heads, dim] contiguous
+ *   lse  fp32 [rows, q_heads] contiguous, or NULL
+ *   causal in {0, 1}; window >= 0 (0: none; only with causal); softcap >= 0,
+ *   finite; scale finite
+ *   workspace  at least mq_cache_attend_workspace_bytes(...) bytes, 256-byte
+ *              aligned (may be NULL when that is 0): partial results of long
+ *              sequences cut into pieces.  Calls that may overlap in time
+ *              need workspaces of their own.
+ * Sizes: q_heads a multiple of heads, q_heads * dim <= 2^20;
+ * max_new * q_heads <= 2^26; rows * q_heads < 2^31; q, out 16-byte aligned,
+ * q_stride a multiple of 8 and >= q_heads * dim.
+ */
+MQ_API size_t mq_cache_attend_workspace_bytes(const mq_kv_cache* cache, const mq_kv_batch* batch,
+                                       int64_t q_heads, int64_t window);
+MQ_API mq_status mq_cache_attend(const mq_kv_cache* cache, const mq_kv_batch* batch,
+                          const uint16_t* q, int64_t q_stride, int64_t q_heads, float scale,
+                          float softcap, int64_t window, int causal, uint16_t* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 
 #ifdef __cplusplus

@@ -35,6 +35,8 @@ EXPORTS = (
     "mq_overflow_rows", "mq_overflow_cols", "mq_overflow_apply", "mq_overflow_apply_grouped",
     "mq_bitplanes_bytes", "mq_pack_bitplanes", "mq_gemv_bitplanes",
     "mq_mlp_workspace_bytes", "mq_mlp_decode",
+    "mq_rope", "mq_cache_append", "mq_cache_read", "mq_cache_attend_workspace_bytes",
+    "mq_cache_attend",
 )
 
 
@@ -137,6 +139,7 @@ def lib() -> ctypes.CDLL:
     L.mq_mixnmatch_forward.argtypes = [ctypes.POINTER(Layer), i32, vp, i64, vp, vp, sz, vp]
     L.mq_mixnmatch_forward_inplace.restype = i32
     L.mq_mixnmatch_forward_inplace.argtypes = [ctypes.POINTER(Layer), i32, vp, i64, vp, sz, vp]
+    declare(L)
     _LIB = L
     return L
 
@@ -582,3 +585,10 @@ def mixnmatch_forward_inplace(layer_arr, h, workspace, stream=None):
                                               _ptr(workspace), ws_bytes, _stream(stream)),
            "mq_mixnmatch_forward_inplace")
     return h
+
+
+# ------------------------------------------------- attention over an 8-bit cache
+
+from .attention import (  # noqa: E402
+    CacheAppendPlan, CacheAttendPlan, KVBatch, KVCache, KV_FORMATS, Rope, RopePlan, cache_append,
+    cache_attend, cache_attend_workspace_bytes, cache_read, declare, rope, rope_frequencies)

@@ -221,6 +221,8 @@ namespace mq {
 
 mq_status record_hip_error(hipError_t e) { return hip_fail(e); }
 
+mq_status device_check() { return check_device(); }
+
 mq_status gemm_check(const uint8_t* packed, int r, const float* alpha, const float* zero,
                      int64_t group, int64_t N, int64_t K, const uint16_t* x, int64_t M,
                      const float* y) {

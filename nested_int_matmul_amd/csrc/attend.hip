@@ -1,0 +1,519 @@
+// Attention over the 8-bit key/value cache.
+//
+//   t_j = scale * <q, k_j> * k_scale(page of j)   (optionally capped)
+//   out = sum_j exp(t_j - m) v_scale v_j / sum_j exp(t_j - m)
+//
+// in one pass over the keys with a running reference m and running sums.
+// Everything is kept transposed (keys x rows, then dims x rows), so that the
+// probabilities leave the first product in the registers where the second
+// one wants them:
+//   S^T [16 keys x 16 rows] = K [16 x dim] Q^T       (A = codes of k)
+//   O^T [16 dims x 16 rows] += V^T [16 x 32 keys] P^T  (A = codes of v)
+// A row is one (token, query head of the group); a lane holds row lane % 16.
+// The order of the keys in a contraction is free as long as both operands
+// agree: MFMA t of a 64-key tile takes as its 16 rows the keys
+// 16 (r / 4) + 4 t + r % 4, which leaves lane group g = lane / 16 with the
+// scores of keys 16 g .. 16 g + 15: all of one page (a page is 16 tokens or
+// more, so one k scale and one v scale a lane), and the 16 consecutive bytes
+// that it loads of each dim of v.  No score and no code goes through LDS.
+//
+// Codes become fp16 exactly (int8 and e4m3 both fit), q becomes fp16 after
+// its row is multiplied by a power of two that brings its largest entry to
+// 2^14 (entries 2^-29 of that and above keep all their bits), the products
+// accumulate in fp32.  Probabilities are rounded to fp16, in units of a
+// reference that stays within 2^8 of the row's maximum: their error is
+// 2^-12 relative, below that of the bf16 result.
+#include "kv_device.h"
+
+namespace mq {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kNoRef = -1e30f;  // reference of a row that has seen no key
+// The reference moves only when a score exceeds it by this much (in log2):
+// exp2 stays below 2^8, far from fp16's 2^16, and most tiles need no
+// exchange between lanes and no rescaling.
+constexpr float kSlack = 8.f;
+
+// 16 codes (as loaded) to two operands of eight fp16.
+template <bool E4M3>
+__device__ __forceinline__ void codes_to_f16(u32x4 w, f16x8* a, f16x8* b) {
+  union {
+    f16x2 h[8];
+    f16x8 v[2];
+  } r;
+  if (E4M3) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.h[2 * i] = __builtin_bit_cast(
+          f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w[i], 1.f, false));
+      r.h[2 * i + 1] = __builtin_bit_cast(
+          f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w[i], 1.f, true));
+    }
+  } else {
+    // byte c + 128 under the fp16 exponent of 1024 is 1152 + c
+    const f16x2 off = {(_Float16)1152.f, (_Float16)1152.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = w[i] ^ 0x80808080u;
+      const uint32_t p0 = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
+      const uint32_t p1 = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
+      r.h[2 * i] = __builtin_bit_cast(f16x2, p0) - off;
+      r.h[2 * i + 1] = __builtin_bit_cast(f16x2, p1) - off;
+    }
+  }
+  *a = r.v[0];
+  *b = r.v[1];
+}
+
+// Keys [lo, hi) of the token at position pos.
+struct Keys {
+  int64_t lo, hi;
+};
+__device__ __forceinline__ Keys keys_of(const AttendArgs& a, int64_t pos, int64_t held) {
+  Keys k;
+  k.hi = a.causal && pos + 1 < held ? pos + 1 : held;
+  k.lo = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
+  if (pos < 0 || k.hi < 0) k.hi = 0;
+  return k;
+}
+
+// What the rows [row_a, row_b) of a (sequence, head) see together, as pieces
+// of a.piece tokens from a 64-aligned start.
+struct Span {
+  int64_t lo, hi;  // lo a multiple of 64; lo >= hi: no key
+  int pieces;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs& a, const SeqSpan& sp, int64_t held,
+                                        int tok_a, int tok_b) {
+  Span r;
+  const Keys f = keys_of(a, sp.start + tok_a, held), l = keys_of(a, sp.start + tok_b, held);
+  r.lo = f.lo & ~(int64_t)63;
+  r.hi = l.hi;
+  r.pieces = r.hi > r.lo ? (int)((r.hi - r.lo + a.piece - 1) / a.piece) : 0;
+  return r;
+}
+__device__ __forceinline__ int64_t held_of(const AttendArgs& a, int s) {
+  const int64_t len = a.batch.kv_len[s];
+  const int64_t room = (int64_t)a.batch.table_pages * a.cache.block;
+  return len < room ? len : room;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------- few rows
+//
+// ROWS * 16 rows a workgroup, NW waves that share them and take the piece's
+// 64-key tiles in turn, each with sums of its own, joined through LDS at the
+// end; pieces are joined by join_kernel.  Bound by the codes' bytes.
+template <int DIM, int ROWS, int NW, bool E4M3, bool CAP>
+__global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
+  constexpr int C = DIM / 64;   // 64-dim chunks of a key
+  constexpr int DT = DIM / 16;  // 16-dim tiles of the output
+  __shared__ float lds_o[NW][16][DIM + 4];
+  __shared__ float lds_ml[NW][ROWS * 16][2];
+
+  const int s = blockIdx.z;
+  const int kvh = blockIdx.x % a.cache.heads;
+  const int row_tile = blockIdx.x / a.cache.heads;
+  const SeqSpan sp = seq_span(a.batch, s);
+  const int rows = sp.n * a.group;  // rows of this sequence and head
+  const int row_base = row_tile * (ROWS * 16);
+  if (row_base >= rows) return;
+  const int row_last = row_base + ROWS * 16 < rows ? row_base + ROWS * 16 - 1 : rows - 1;
+  const int64_t held = held_of(a, s);
+  const Span span = span_of(a, sp, held, row_base / a.group, row_last / a.group);
+  const int piece = blockIdx.y;
+  if (piece > 0 && piece >= span.pieces) return;
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 4, r16 = lane & 15;
+
+  // ---- this lane's rows: the queries as fp16, and the keys they see
+  f16x8 q[ROWS][C][2];
+  float qf[ROWS];
+  int64_t see_lo[ROWS], see_hi[ROWS];
+#pragma unroll
+  for (int rt = 0; rt < ROWS; ++rt) {
+    const int row = row_base + rt * 16 + r16;
+    const bool real = row < rows;
+    const int tok = real ? row / a.group : 0;
+    const int head = kvh * a.group + (real ? row - tok * a.group : 0);
+    const uint16_t* qp = a.q + (int64_t)(sp.row0 + tok) * a.q_stride + (int64_t)head * DIM;
+    u32x4 raw[C][2];
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        raw[c][h] = real ? *reinterpret_cast<const u32x4*>(qp + 64 * c + 16 * g + 8 * h)
+                         : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t x = raw[c][h][e] & 0x7fffu, y = (raw[c][h][e] >> 16) & 0x7fffu;
+          top = x > top ? x : top;
+          top = y > top ? y : top;
+        }
+      }
+    uint32_t o = __shfl_xor(top, 16);
+    top = o > top ? o : top;
+    o = __shfl_xor(top, 32);
+    top = o > top ? o : top;
+    int e = (int)(top >> 7) - 127;       // exponent of the row's largest entry
+    e = e < -100 ? -100 : (e > 127 ? 14 : e);  // (no scaling of rows with inf or NaN)
+    const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+    qf[rt] = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * a.scale;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t pair = raw[c][h][j >> 1];
+          const float x = __uint_as_float((j & 1) ? pair & 0xffff0000u : pair << 16);
+          q[rt][c][h][j] = (_Float16)(x * up);
+        }
+    const Keys k = keys_of(a, sp.start + tok, held);
+    see_lo[rt] = k.lo;
+    see_hi[rt] = real ? k.hi : 0;
+  }
+  // keys that every real row sees: no mask needed there
+  const Keys first = keys_of(a, sp.start + row_base / a.group, held);
+  const Keys last = keys_of(a, sp.start + row_last / a.group, held);
+
+  f32x4 acc[ROWS][DT];
+  float ref[ROWS], sum[ROWS];
+#pragma unroll
+  for (int rt = 0; rt < ROWS; ++rt) {
+    ref[rt] = kNoRef;
+    sum[rt] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[rt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  float vref = 0.f, vinv = 0.f;  // unit of the v scales in acc
+
+  const int64_t begin = span.lo + (int64_t)piece * a.piece;
+  const int64_t stop = begin + a.piece < span.hi ? begin + a.piece : span.hi;
+  const int block = a.cache.block;
+  const int shift = __builtin_ctz(block);
+  const int64_t page_bytes = (int64_t)block * DIM;
+  const float log_scale = kLog2e;
+
+  for (int64_t key0 = begin + 64 * wave; key0 < stop; key0 += 64 * NW) {
+    // pages of the 16 keys whose v this lane loads (and whose scores it gets),
+    // and of the keys whose k it loads
+    const int64_t kv0 = key0 + 16 * g, kk0 = key0 + 16 * (r16 >> 2);
+    const int pv = kv0 < stop ? page_of(a.batch, s, kv0 >> shift, a.cache.pages) : -1;
+    const int pk = kk0 < stop ? page_of(a.batch, s, kk0 >> shift, a.cache.pages) : -1;
+    const bool masked = key0 < last.lo || key0 + 64 > first.hi || key0 + 64 > stop ||
+                        __any(pv < 0);
+    const int64_t phv = (int64_t)(pv < 0 ? 0 : pv) * a.cache.heads + kvh;
+    const int64_t phk = (int64_t)(pk < 0 ? 0 : pk) * a.cache.heads + kvh;
+    const uint8_t* kp = a.cache.k + phk * page_bytes +
+                        ((kk0 & (block - 1)) + (r16 & 3)) * DIM + 16 * g;
+    const uint8_t* vp = a.cache.v + phv * page_bytes + (int64_t)r16 * block + (kv0 & (block - 1));
+    const float ks = a.cache.k_scale[phv];
+    float vs = a.cache.v_scale[phv];
+    u32x4 kc[4][C], vc[DT];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        kc[t][c] = *reinterpret_cast<const u32x4*>(kp + 4 * t * DIM + 64 * c);
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+      vc[d] = *reinterpret_cast<const u32x4*>(vp + (int64_t)16 * d * block);
+
+    // ---- scores
+    f32x4 sc[ROWS][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int rt = 0; rt < ROWS; ++rt) sc[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        f16x8 lo, hi;
+        codes_to_f16<E4M3>(kc[t][c], &lo, &hi);
+#pragma unroll
+        for (int rt = 0; rt < ROWS; ++rt) {
+          sc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, q[rt][c][0], sc[rt][t], 0, 0, 0);
+          sc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, q[rt][c][1], sc[rt][t], 0, 0, 0);
+        }
+      }
+    }
+    // ---- mask: keys beyond the sequence, and bytes there (never written)
+    // must not reach the products as NaN
+    int live = 16;  // of this lane's 16 keys, those that are held
+    if (masked) {
+      const int64_t n = stop - kv0;
+      live = pv < 0 || n <= 0 ? 0 : (n < 16 ? (int)n : 16);
+      if (live == 0) vs = 0.f;
+    }
+    // ---- unit of v
+    if (__any(vs > vref)) {
+      float m = vs;
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      m = fmaxf(m, vref);
+      const float f = vref / m;
+#pragma unroll
+      for (int rt = 0; rt < ROWS; ++rt)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[rt][d] = acc[rt][d] * f;
+      vref = m;
+      vinv = 1.f / m;
+    }
+    const float vw = vs * vinv;
+    // ---- probabilities
+    f16x8 p[ROWS][2];
+#pragma unroll
+    for (int rt = 0; rt < ROWS; ++rt) {
+      const float f = CAP ? ks * qf[rt] : ks * qf[rt] * log_scale;
+      float x[16];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y = sc[rt][t][i] * f;
+          if (CAP) {
+            // tanh(z) = 1 - 2 / (e^2z + 1), by its series where that cancels
+            const float z = y / a.softcap;
+            const float e2 = __builtin_amdgcn_exp2f(2.f * kLog2e * fabsf(z));
+            const float big = copysignf(1.f - 2.f / (e2 + 1.f), z);
+            const float zz = z * z;
+            const float small =
+                z * (1.f + zz * (-1.f / 3.f + zz * (2.f / 15.f + zz * (-17.f / 315.f))));
+            y = (fabsf(z) < 0.125f ? small : big) * (a.softcap * kLog2e);
+          }
+          x[4 * t + i] = y;
+        }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int64_t j = kv0 + i;
+          if (i >= live || j < see_lo[rt] || j >= see_hi[rt]) x[i] = -INFINITY;
+        }
+      }
+      float top = x[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+      if (__any(top > ref[rt] + kSlack)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float m = fmaxf(top, ref[rt]);
+        const float f2 = __builtin_amdgcn_exp2f(ref[rt] - m);
+        ref[rt] = m;
+        sum[rt] *= f2;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[rt][d] = acc[rt][d] * f2;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float e = __builtin_amdgcn_exp2f(x[i] - ref[rt]);
+        sum[rt] += e;
+        p[rt][i >> 3][i & 7] = (_Float16)(e * vw);
+      }
+    }
+    if (masked && E4M3) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int keep = live - 4 * e;
+          vc[d][e] &= keep >= 4 ? 0xffffffffu : (keep <= 0 ? 0u : (1u << (8 * keep)) - 1);
+        }
+    }
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      f16x8 lo, hi;
+      codes_to_f16<E4M3>(vc[d], &lo, &hi);
+#pragma unroll
+      for (int rt = 0; rt < ROWS; ++rt) {
+        acc[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, p[rt][0], acc[rt][d], 0, 0, 0);
+        acc[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, p[rt][1], acc[rt][d], 0, 0, 0);
+      }
+    }
+  }
+
+  // ---- join the waves: reference and sum of every row, then the outputs
+#pragma unroll
+  for (int rt = 0; rt < ROWS; ++rt) {
+    sum[rt] += __shfl_xor(sum[rt], 16);
+    sum[rt] += __shfl_xor(sum[rt], 32);
+    if (g == 0) {
+      lds_ml[wave][rt * 16 + r16][0] = ref[rt];
+      lds_ml[wave][rt * 16 + r16][1] = sum[rt];
+    }
+  }
+  __syncthreads();
+  const bool direct = span.pieces <= 1;
+#pragma unroll
+  for (int rt = 0; rt < ROWS; ++rt) {
+    float m = kNoRef, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) m = fmaxf(m, lds_ml[w][rt * 16 + r16][0]);
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+      l += lds_ml[w][rt * 16 + r16][1] * __builtin_amdgcn_exp2f(lds_ml[w][rt * 16 + r16][0] - m);
+    // (a NaN reference cannot be: fmaxf drops it; its sum is NaN)
+    const float f = __builtin_amdgcn_exp2f(ref[rt] - m) * vref;
+    if (rt > 0) __syncthreads();
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const f32x4 o = acc[rt][d] * f;
+      *reinterpret_cast<f32x4*>(&lds_o[wave][r16][16 * d + 4 * g]) = o;
+    }
+    __syncthreads();
+    // 16 rows x DIM outputs over NW * 64 threads, four at a time
+    for (int i = threadIdx.x; i < 16 * (DIM / 4); i += NW * 64) {
+      const int rr = i / (DIM / 4), d = (i % (DIM / 4)) * 4;
+      const int row = row_base + rt * 16 + rr;
+      if (row >= rows) continue;
+      f32x4 o = *reinterpret_cast<f32x4*>(&lds_o[0][rr][d]);
+#pragma unroll
+      for (int w = 1; w < NW; ++w) o = o + *reinterpret_cast<f32x4*>(&lds_o[w][rr][d]);
+      float mm = kNoRef, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) mm = fmaxf(mm, lds_ml[w][rt * 16 + rr][0]);
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+        ll += lds_ml[w][rt * 16 + rr][1] * __builtin_amdgcn_exp2f(lds_ml[w][rt * 16 + rr][0] - mm);
+      const int tok = row / a.group;
+      const int64_t out_row =
+          (int64_t)(sp.row0 + tok) * a.q_heads + kvh * a.group + (row - tok * a.group);
+      if (direct) {
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        u32x2 b;
+        b[0] = bf16_rne(o[0] * inv) | (bf16_rne(o[1] * inv) << 16);
+        b[1] = bf16_rne(o[2] * inv) | (bf16_rne(o[3] * inv) << 16);
+        if (ll == 0.f) b = u32x2{0, 0};
+        *reinterpret_cast<u32x2*>(a.out + out_row * DIM + d) = b;
+        if (a.lse && d == 0) a.lse[out_row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      } else {
+        const int64_t at = (int64_t)piece * a.batch.rows * a.q_heads + out_row;
+        *reinterpret_cast<f32x4*>(a.part_o + at * DIM + d) = o;
+        if (d == 0) {
+          a.part_ml[2 * at] = mm;
+          a.part_ml[2 * at + 1] = ll;
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------- the join
+//
+// One wave a row: the pieces' references and sums, then their outputs.
+template <int DIM>
+__global__ void __launch_bounds__(256) join_kernel(AttendArgs a, int tile_rows) {
+  constexpr int E = DIM / 64;
+  const int s = blockIdx.z;
+  const int kvh = blockIdx.y;
+  const SeqSpan sp = seq_span(a.batch, s);
+  const int rows = sp.n * a.group;
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  const int64_t held = held_of(a, s);
+  const int row_base = row / tile_rows * tile_rows;
+  const int row_last = row_base + tile_rows < rows ? row_base + tile_rows - 1 : rows - 1;
+  const Span span = span_of(a, sp, held, row_base / a.group, row_last / a.group);
+  if (span.pieces <= 1) return;  // written already
+  const int lane = threadIdx.x & 63;
+  const int tok = row / a.group;
+  const int64_t out_row =
+      (int64_t)(sp.row0 + tok) * a.q_heads + kvh * a.group + (row - tok * a.group);
+  const int64_t step = a.batch.rows * a.q_heads;
+  float m = kNoRef;
+  for (int i = lane; i < span.pieces; i += 64) m = fmaxf(m, a.part_ml[2 * (out_row + i * step)]);
+  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+  float l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int i = 0; i < span.pieces; ++i) {
+    const int64_t at = out_row + i * step;
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - m);
+    l += a.part_ml[2 * at + 1] * f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] += a.part_o[at * DIM + lane * E + e] * f;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    a.out[out_row * DIM + lane * E + e] = l == 0.f ? 0 : (uint16_t)bf16_rne(o[e] * inv);
+  if (a.lse && lane == 0) a.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+namespace {
+
+// Rows of a workgroup for max_new tokens of `group` heads each.
+int rows_tile(int64_t most_rows) { return most_rows <= 16 ? 16 : 32; }
+constexpr int kFewWaves = 4;
+
+template <int DIM, int ROWS, int NW>
+hipError_t few(const AttendArgs& a, dim3 grid, hipStream_t s) {
+  const dim3 block(NW * 64);
+  const bool cap = a.softcap > 0.f;
+  if (a.cache.e4m3) {
+    if (cap)
+      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, NW, true, true>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, NW, true, false>), grid, block, 0, s, a);
+  } else {
+    if (cap)
+      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, NW, false, true>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, NW, false, false>), grid, block, 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+template <int DIM>
+hipError_t attend_dim(AttendArgs& a, hipStream_t s) {
+  const int64_t most = (int64_t)a.batch.max_new * a.group;
+  const int tile = rows_tile(most);
+  const dim3 grid((unsigned)(a.cache.heads * ((most + tile - 1) / tile)), (unsigned)a.pieces,
+                  (unsigned)a.batch.seqs);
+  hipError_t e = tile == 16 ? few<DIM, 1, kFewWaves>(a, grid, s) : few<DIM, 2, kFewWaves>(a, grid, s);
+  if (e != hipSuccess || a.pieces <= 1) return e;
+  const dim3 jg((unsigned)((most + 3) / 4), (unsigned)a.cache.heads, (unsigned)a.batch.seqs);
+  hipLaunchKernelGGL((join_kernel<DIM>), jg, dim3(256), 0, s, a, tile);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attend_plan(AttendArgs& a) {
+  const int64_t most = (int64_t)a.batch.max_new * a.group;
+  const int tile = rows_tile(most);
+  int64_t keys = (int64_t)a.batch.table_pages * a.cache.block;
+  if (a.window > 0 && a.window + a.batch.max_new + 64 < keys)
+    keys = a.window + a.batch.max_new + 64;
+  const int64_t groups = (int64_t)a.batch.seqs * a.cache.heads * ((most + tile - 1) / tile);
+  int64_t pieces = 2048 / groups;
+  if (pieces < 1) pieces = 1;
+  int64_t piece = (keys + pieces - 1) / pieces;
+  const int64_t least = 64 * kFewWaves;
+  piece = (piece + least - 1) / least * least;
+  a.piece = (int)piece;
+  a.pieces = (int)((keys + piece - 1) / piece);
+  if (a.pieces <= 1) {
+    a.pieces = 1;
+    return 0;
+  }
+  return (size_t)a.pieces * a.batch.rows * a.q_heads * (a.cache.dim + 2) * sizeof(float);
+}
+
+hipError_t launch_attend(AttendArgs& a, hipStream_t s) {
+  if (a.batch.rows == 0) return hipSuccess;
+  switch (a.cache.dim) {
+    case 64: return attend_dim<64>(a, s);
+    case 128: return attend_dim<128>(a, s);
+    case 256: return attend_dim<256>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace mq

@@ -1,0 +1,227 @@
+// Device-side helpers of the 8-bit key/value cache and the rotary positions.
+#pragma once
+
+#include "mq_device.h"
+#include "mq_internal.h"
+
+namespace mq {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// Smallest scale of a page with codes other than 0.  Above it the remainder
+// of a division by the scale stays a normal fp32 number (see exact_quotient).
+constexpr float kMinScale = 0x1p-100f;
+
+// 1 / (largest code) as fp32
+__device__ __forceinline__ float kv_inv_qmax(bool e4m3) { return e4m3 ? 1.f / 448.f : 1.f / 127.f; }
+
+// One sequence's tokens of a call: rows [row0, row0 + n), positions
+// [start, start + n), cut to what the batch's sizes allow.
+struct SeqSpan {
+  int row0, n;
+  int64_t start;
+};
+__device__ __forceinline__ SeqSpan seq_span(const KvBatch& b, int s) {
+  SeqSpan r;
+  const int64_t a = b.q_start[s], e = b.q_start[s + 1];
+  const int64_t lo = a < 0 ? 0 : (a > b.rows ? b.rows : a);
+  const int64_t hi = e < lo ? lo : (e > b.rows ? b.rows : e);
+  r.row0 = (int)lo;
+  r.n = (int)(hi - lo);
+  r.start = (int64_t)b.kv_len[s] - r.n;
+  if (r.n > b.max_new) r.n = b.max_new;
+  return r;
+}
+
+// Physical page of a position's page index, or -1 where none is held.
+__device__ __forceinline__ int page_of(const KvBatch& b, int s, int64_t pi, int pages) {
+  if (pi < 0 || pi >= b.table_pages) return -1;
+  const int p = b.page_table[(int64_t)s * b.table_pages + pi];
+  return (p < 0 || p >= pages) ? -1 : p;
+}
+
+// ---- rounding to codes
+// x / s rounded to odd at fp32: the quotient cut towards zero, its last bit
+// set if anything was cut.  A later rounding to fewer bits then equals the
+// rounding of the exact quotient.  rs = 1 / s.  One correction step brings
+// the first estimate within an ulp; the remainder's sign (exact in one fma:
+// s >= 2^-100 keeps it normal wherever a code is near a border) says on which
+// side the quotient lies.
+__device__ __forceinline__ float exact_quotient(float x, float s, float rs) {
+  float y = x * rs;
+  y = fmaf(fmaf(-y, s, x), rs, y);
+  const float rem = fmaf(-y, s, x);
+  int bits = __float_as_int(y);
+  // remainder against the quotient's sign: |x / s| < |y|
+  if (rem != 0.f) {
+    if ((__float_as_int(rem) ^ __float_as_int(x)) < 0) bits -= 1;
+    bits |= 1;
+  }
+  return __int_as_float(bits);
+}
+
+// fp64 -> fp32 rounded to odd
+__device__ __forceinline__ float f64_to_f32_odd(double q) {
+  const float f = (float)q;
+  int bits = __float_as_int(f);
+  if ((double)f != q) {
+    if (fabs((double)f) > fabs(q)) bits -= 1;
+    bits |= 1;
+  }
+  return __int_as_float(bits);
+}
+
+// Four quotients (rounded to odd) to four code bytes.
+__device__ __forceinline__ uint32_t codes_of(const float* y, bool e4m3) {
+  if (e4m3) {
+    float c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = fminf(fmaxf(y[i], -448.f), 448.f);
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
+  }
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = (int)__builtin_rintf(fminf(fmaxf(y[i], -127.f), 127.f));
+    w |= ((uint32_t)c & 0xffu) << (8 * i);
+  }
+  return w;
+}
+
+// The number a code byte stands for (without the scale).
+__device__ __forceinline__ void numbers_of(uint32_t w, bool e4m3, float* y) {
+  if (e4m3) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+    const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    y[0] = a[0]; y[1] = a[1]; y[2] = b[0]; y[3] = b[1];
+  } else {
+    y[0] = (float)(int8_t)(w & 0xffu);
+    y[1] = (float)(int8_t)((w >> 8) & 0xffu);
+    y[2] = (float)(int8_t)((w >> 16) & 0xffu);
+    y[3] = (float)(int8_t)(w >> 24);
+  }
+}
+
+// Four code bytes whose page's scale grows from `was` to `now`.
+__device__ __forceinline__ uint32_t recode(uint32_t w, bool e4m3, double was, double now) {
+  float y[4];
+  numbers_of(w, e4m3, y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float q = f64_to_f32_odd((double)y[i] * was / now);
+    y[i] = q == q ? q : 0.f;
+  }
+  return codes_of(y, e4m3);
+}
+
+// ---- rotary positions
+// sin and cos of a in float64.  a is reduced by the nearest multiple k of
+// pi/2, with pi/2 as a sum of two float64 (k * hi is exact within the fma, and
+// k * lo is below 2^-22 for |k| < 2^32, so the reduction adds less than half
+// an ulp of 1); on |r| <= pi/4 the Taylor series to r^17 and r^16 are cut
+// below 2^-60.
+__device__ __forceinline__ void sincos64(double a, double* s, double* c) {
+  const double k = rint(a * 0.63661977236758134308);  // 2 / pi
+  double r = fma(-k, 1.57079632679489655800, a);      // pi/2, upper 53 bits
+  r = fma(-k, 6.12323399573676603587e-17, r);         // pi/2, the rest
+  const double z = r * r;
+  double p = 1.0 / 355687428096000.0;                 // 1 / 17!
+  p = fma(p, z, -1.0 / 1307674368000.0);
+  p = fma(p, z, 1.0 / 6227020800.0);
+  p = fma(p, z, -1.0 / 39916800.0);
+  p = fma(p, z, 1.0 / 362880.0);
+  p = fma(p, z, -1.0 / 5040.0);
+  p = fma(p, z, 1.0 / 120.0);
+  p = fma(p, z, -1.0 / 6.0);
+  const double sn = fma(p * z, r, r);
+  double q = 1.0 / 20922789888000.0;                  // 1 / 16!
+  q = fma(q, z, -1.0 / 87178291200.0);
+  q = fma(q, z, 1.0 / 479001600.0);
+  q = fma(q, z, -1.0 / 3628800.0);
+  q = fma(q, z, 1.0 / 40320.0);
+  q = fma(q, z, -1.0 / 720.0);
+  q = fma(q, z, 1.0 / 24.0);
+  q = fma(q, z, -0.5);
+  const double cs = fma(q, z, 1.0);
+  const long long m = (long long)k;
+  const double s0 = (m & 1) ? cs : sn, c0 = (m & 1) ? sn : cs;
+  *s = (m & 2) ? -s0 : s0;
+  *c = ((m + 1) & 2) ? -c0 : c0;
+}
+
+// A thread's unit of a head: eight entries as two runs of four, [lo, lo + 4)
+// and [hi, hi + 4).  In the rotated part the unit holds four pairs; pairs()
+// gives the first pair's index.
+struct Unit {
+  int lo, hi, pair0;
+  bool turns;
+};
+__device__ __forceinline__ Unit unit_of(int u, int rot, bool interleaved) {
+  Unit r;
+  r.turns = u * 8 < rot;
+  r.pair0 = 4 * u;
+  if (r.turns && !interleaved) {
+    r.lo = 4 * u;
+    r.hi = rot / 2 + 4 * u;
+  } else {
+    r.lo = 8 * u;
+    r.hi = 8 * u + 4;
+  }
+  return r;
+}
+
+// The unit's eight entries, from bf16 or fp32.
+__device__ __forceinline__ void load_unit(const void* x, bool f32, int64_t at, const Unit& u,
+                                          float* v) {
+  if (f32) {
+    const float* p = static_cast<const float*>(x) + at;
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p + u.lo);
+    const f32x4 b = *reinterpret_cast<const f32x4*>(p + u.hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(x) + at;
+    const u32x2 a = *reinterpret_cast<const u32x2*>(p + u.lo);
+    const u32x2 b = *reinterpret_cast<const u32x2*>(p + u.hi);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+      v[4 + 2 * i] = __uint_as_float(b[i] << 16);
+      v[4 + 2 * i + 1] = __uint_as_float(b[i] & 0xffff0000u);
+    }
+  }
+}
+
+// Turn the unit's four pairs by (c, s) in float64, each result rounded once
+// to fp32.
+__device__ __forceinline__ void turn_unit(float* v, const double* c, const double* s,
+                                          bool interleaved) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int i1 = interleaved ? 2 * i : i, i2 = interleaved ? 2 * i + 1 : 4 + i;
+    const double x1 = v[i1], x2 = v[i2];
+    v[i1] = (float)(x1 * c[i] - x2 * s[i]);
+    v[i2] = (float)(x2 * c[i] + x1 * s[i]);
+  }
+}
+
+// fp32 -> bf16 bits, nearest even; NaN stays a NaN.
+__device__ __forceinline__ uint32_t bf16_rne(float f) {
+  const uint32_t u = __float_as_uint(f);
+  const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+  return (u & 0x7fffffffu) > 0x7f800000u ? ((u >> 16) | 0x40u) : r;
+}
+// Four dwords of bf16 pairs: the unit's lo run in w[0..1], its hi run in w[2..3].
+__device__ __forceinline__ void pack_unit(const float* v, uint32_t* w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = bf16_rne(v[2 * i]) | (bf16_rne(v[2 * i + 1]) << 16);
+}
+
+}  // namespace mq

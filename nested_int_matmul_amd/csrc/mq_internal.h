@@ -132,4 +132,53 @@ hipError_t launch_gemv_bitplanes(const uint8_t* planes, int r, bool extra, const
                                  const float* zero, int64_t group, int64_t N, int64_t K,
                                  const uint16_t* x, int64_t M, float* y, hipStream_t s);
 
+// Attention over the 8-bit cache (kv_cache.hip, attend.hip).  Kernel-side
+// copies of the C structs.
+struct KvCache {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  int pages, heads, block, dim;
+  int e4m3;
+};
+struct KvBatch {
+  const int *q_start, *kv_len, *page_table;
+  int64_t rows;
+  int seqs, table_pages, max_new;
+};
+struct RopeSpec {
+  const double* freq;  // nullptr: no rotation
+  double factor;
+  int rot, interleaved;
+};
+struct AttendArgs {
+  KvCache cache;
+  KvBatch batch;
+  const uint16_t* q;
+  int64_t q_stride;
+  int group, q_heads;
+  float scale, softcap;
+  int64_t window;
+  int causal;
+  uint16_t* out;
+  float* lse;
+  float* part_o;  // fp32 [pieces][rows][q_heads][dim]
+  float* part_ml; // fp32 [pieces][rows][q_heads][2]
+  int piece;      // tokens of one piece
+  int pieces;     // most pieces of a row (1: no workspace)
+};
+hipError_t launch_rope(const RopeSpec& r, const int* positions, const void* x, bool f32,
+                       int64_t x_stride, int64_t rows, int heads, int dim, uint16_t* out,
+                       int64_t out_stride, hipStream_t s);
+hipError_t launch_cache_append(const KvCache& c, const KvBatch& b, const RopeSpec& r,
+                               const void* k, const void* v, int64_t kv_stride, const void* q,
+                               int64_t q_stride, int q_heads, bool f32, uint16_t* q_out,
+                               hipStream_t s);
+hipError_t launch_cache_read(const KvCache& c, const KvBatch& b, void* k_out, void* v_out,
+                             bool f32, hipStream_t s);
+// Bytes of partial results; fills piece and pieces.
+size_t attend_plan(AttendArgs& a);
+hipError_t launch_attend(AttendArgs& a, hipStream_t s);
+// MQ_OK if the current device is a gfx950.
+mq_status device_check();
+
 }  // namespace mq
