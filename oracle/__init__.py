@@ -36,3 +36,11 @@ from .matquant import (  # noqa: F401
     unpack_bitplanes,
     unpack_indices,
 )
+from .attention import (  # noqa: F401
+    Cache,
+    E4M3,
+    numbers,
+    rope_turn,
+    round_codes,
+    to_bf16,
+)
