@@ -552,6 +552,43 @@ MQ_API mq_status mq_cache_attend(const mq_kv_cache* cache, const mq_kv_batch* ba
                           float softcap, int64_t window, int causal, uint16_t* out, float* lse,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The Mix'n'Match stack with attention: the layers of mq_mixnmatch_forward
+ * with the attention between their projections and W_o,
+ *   a = bf16(h / sqrt(mean(h^2)));  q, k, v, u, g = W a   (fp32)
+ *   q' = bf16(rope(q));  k, v are appended to the layer's cache (k rotated)
+ *   o = W_o attend(q', cache),  d = W_down bf16(u * g),  h = h + o + d.
+ * Row m of x and h_out is row m of `batch` (batch.rows == M <= 8: one token
+ * of several sequences, several of one, or both).  Rows that belong to no
+ * sequence get unspecified values.
+ *   caches   HOST array [n_layers]: one cache a layer, same heads, dim, block,
+ *            with heads * dim = Hkv (rows of k and v) and q_heads * dim = H
+ *   batch    as for mq_cache_append; the layers share the page table
+ *   rope     NULL: no rotation
+ *   windows  HOST array [n_layers] of window sizes (0: none), or NULL: none
+ * `attn` and its host arrays are read during the call only.
+ */
+typedef struct mq_stack_attention {
+  const mq_kv_cache* caches;
+  const mq_kv_batch* batch;
+  const mq_rope_spec* rope;
+  const int64_t* windows;
+  int64_t q_heads;
+  float scale, softcap;
+} mq_stack_attention;
+
+/* Workspace bytes (0 on invalid arguments).  The first
+ * mq_mixnmatch_workspace_bytes of it hold the last layer's intermediates as
+ * mq_mixnmatch_workspace_offsets describes them (bf16(q) is the rotated q');
+ * then, at the next multiple of 256, the attention's output (bf16 [M, H]). */
+MQ_API size_t mq_mixnmatch_attend_workspace_bytes(const mq_layer* layers, int n_layers,
+                                           const mq_stack_attention* attn, int64_t M);
+/* x: bf16 [M, H], or NULL: h holds the residual stream (fp32 [M, H]) on
+ * entry and the layers continue it.  Otherwise as mq_mixnmatch_forward. */
+MQ_API mq_status mq_mixnmatch_attend(const mq_layer* layers, int n_layers,
+                              const mq_stack_attention* attn, const uint16_t* x, int64_t M,
+                              float* h, void* workspace, size_t workspace_bytes, void* stream);
+
 
 #ifdef __cplusplus
 }

@@ -36,7 +36,7 @@ EXPORTS = (
     "mq_bitplanes_bytes", "mq_pack_bitplanes", "mq_gemv_bitplanes",
     "mq_mlp_workspace_bytes", "mq_mlp_decode",
     "mq_rope", "mq_cache_append", "mq_cache_read", "mq_cache_attend_workspace_bytes",
-    "mq_cache_attend",
+    "mq_cache_attend", "mq_mixnmatch_attend_workspace_bytes", "mq_mixnmatch_attend",
 )
 
 
@@ -590,5 +590,6 @@ def mixnmatch_forward_inplace(layer_arr, h, workspace, stream=None):
 # ------------------------------------------------- attention over an 8-bit cache
 
 from .attention import (  # noqa: E402
-    CacheAppendPlan, CacheAttendPlan, KVBatch, KVCache, KV_FORMATS, Rope, RopePlan, cache_append,
-    cache_attend, cache_attend_workspace_bytes, cache_read, declare, rope, rope_frequencies)
+    CacheAppendPlan, CacheAttendPlan, KVBatch, KVCache, KV_FORMATS, Rope, RopePlan,
+    StackAttention, cache_append, cache_attend, cache_attend_workspace_bytes, cache_read, declare,
+    mixnmatch_attend, mixnmatch_attend_workspace_bytes, rope, rope_frequencies)

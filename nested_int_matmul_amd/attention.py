@@ -47,6 +47,13 @@ class _RopeSpec(ctypes.Structure):
                 ("interleaved", ctypes.c_int32)]
 
 
+class _StackAttention(ctypes.Structure):
+    _fields_ = [("caches", ctypes.POINTER(_Cache)), ("batch", ctypes.POINTER(_Batch)),
+                ("rope", ctypes.POINTER(_RopeSpec)), ("windows", ctypes.POINTER(ctypes.c_int64)),
+                ("q_heads", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float)]
+
+
 def declare(L):
     """Signatures of this module's entry points (called by lib())."""
     i64, vp, i32, sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -62,6 +69,11 @@ def declare(L):
     L.mq_cache_attend_workspace_bytes.argtypes = [C, B, i64, i64]
     L.mq_cache_attend.restype = i32
     L.mq_cache_attend.argtypes = [C, B, vp, i64, i64, f32, f32, i64, i32, vp, vp, vp, sz, vp]
+    A = ctypes.POINTER(_StackAttention)
+    L.mq_mixnmatch_attend_workspace_bytes.restype = sz
+    L.mq_mixnmatch_attend_workspace_bytes.argtypes = [vp, i32, A, i64]
+    L.mq_mixnmatch_attend.restype = i32
+    L.mq_mixnmatch_attend.argtypes = [vp, i32, A, vp, i64, vp, vp, sz, vp]
 
 
 # ---------------------------------------------------------------- argument checks
@@ -402,3 +414,62 @@ def cache_attend(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float =
                            stream)
     plan()
     return plan.result if lse is None else plan.result[0]
+
+
+class StackAttention:
+    """The attention of a Mix'n'Match stack: one KVCache a layer (same heads,
+    dim and block), the batch that its rows belong to, the positions and, per
+    layer, a window (0: none)."""
+
+    def __init__(self, caches, batch: KVBatch, q_heads: int, rope: Rope = None, scale=None,
+                 softcap: float = 0.0, windows=None):
+        self.caches, self.batch, self.rope = list(caches), batch, rope
+        if not self.caches:
+            raise ValueError("mq: one cache a layer")
+        if windows is not None and len(windows) != len(self.caches):
+            raise ValueError("mq: one window a layer")
+        self.q_heads = int(q_heads)
+        _same_device(batch.q_start, rope.freq if rope else None, *(c.k for c in self.caches))
+        self._arr = (_Cache * len(self.caches))(*(c.c for c in self.caches))
+        self._win = None if windows is None else (ctypes.c_int64 * len(windows))(*windows)
+        self.c = _StackAttention(
+            self._arr, ctypes.pointer(batch.c), ctypes.pointer(rope.spec) if rope else None,
+            self._win, self.q_heads,
+            float(self.caches[0].dim ** -0.5 if scale is None else scale), float(softcap))
+
+
+def mixnmatch_attend_workspace_bytes(layer_arr, attn: StackAttention, M: int) -> int:
+    if len(layer_arr) != len(attn.caches):
+        raise ValueError("mq: one cache a layer")
+    return int(lib().mq_mixnmatch_attend_workspace_bytes(layer_arr, len(layer_arr),
+                                                         ctypes.byref(attn.c), M))
+
+
+def mixnmatch_attend(layer_arr, attn: StackAttention, x=None, h=None, workspace=None, stream=None):
+    """Run the stack with attention on bf16 x [M, H] (row m is row m of the
+    attention's batch): returns the fp32 residual stream h [M, H].  Without x
+    the layers continue the residual stream h, in place."""
+    import torch
+
+    if x is None and h is None:
+        raise ValueError("mq: x or h is needed")
+    m, H = (x if x is not None else h).shape
+    width = int(layer_arr[0].q.N) if len(layer_arr) else 0
+    if H != width or m != attn.batch.rows:
+        raise ValueError(f"mq: the input is [{m}, {H}], expected [{attn.batch.rows}, {width}]")
+    dev = (x if x is not None else h).device
+    if x is not None:
+        _need(x, "x", (torch.bfloat16, torch.int16, torch.uint16), shape=(m, H))
+    if h is None:
+        h = _empty((m, H), torch.float32, dev, stream)
+    _need(h, "h", (torch.float32,), shape=(m, H))
+    need = mixnmatch_attend_workspace_bytes(layer_arr, attn, m)
+    if workspace is None:
+        workspace = _empty((max(need, 1),), torch.uint8, dev, stream)
+    _need(workspace, "workspace", (torch.uint8,))
+    _same_device(x, h, workspace, attn.batch.q_start)
+    _on_current(h, stream)
+    _check(lib().mq_mixnmatch_attend(layer_arr, len(layer_arr), ctypes.byref(attn.c), _ptr(x), m,
+                                     _ptr(h), _ptr(workspace), workspace.numel(),
+                                     _stream(stream)), "mq_mixnmatch_attend")
+    return h

@@ -461,10 +461,50 @@ mq_status mq_mixnmatch_workspace_offsets(const mq_layer* layers, int n_layers, i
 
 namespace {
 
-// The layer loop of both stack entry points.  x == nullptr: h holds the
-// residual stream on entry; else h = x (bf16) first.
-mq_status run_stack(const mq_layer* layers, int n_layers, const uint16_t* x, float* h, int64_t M,
-                    void* workspace, size_t workspace_bytes, hipStream_t st) {
+int64_t window_of(const mq_stack_attention& at, int layer) {
+  return at.windows ? at.windows[layer] : 0;
+}
+
+// Checks of the attention of a stack, every layer's (the addresses stand for
+// 16-byte aligned parts of the workspace).
+mq_status check_stack_attention(const mq_stack_attention* at, int n_layers, const StackDims& d,
+                                int64_t M) {
+  if (!at || !at->caches || !at->batch) return MQ_ERR_NULL;
+  if (at->batch->rows != M) return MQ_ERR_SHAPE;
+  const auto* part = reinterpret_cast<const uint16_t*>((uintptr_t)256);
+  for (int i = 0; i < n_layers; ++i) {
+    const mq_kv_cache& c = at->caches[i];
+    if (c.heads != at->caches[0].heads || c.dim != at->caches[0].dim ||
+        c.block != at->caches[0].block)
+      return MQ_ERR_SHAPE;
+    mq_status s = mq::append_check(&c, at->batch, at->rope, part, part, d.Hkv, part, d.H,
+                                   at->q_heads, MQ_F32, part);
+    if (s != MQ_OK) return s;
+    s = mq::attend_check(&c, at->batch, part, d.H, at->q_heads, at->scale, at->softcap,
+                         window_of(*at, i), 1, part, nullptr);
+    if (s != MQ_OK) return s;
+    if ((int64_t)c.heads * c.dim != d.Hkv || at->q_heads * c.dim != d.H) return MQ_ERR_SHAPE;
+  }
+  return MQ_OK;
+}
+
+// Bytes of the attention's scratch, the most of any layer.
+size_t stack_attention_scratch(const mq_stack_attention& at, int n_layers) {
+  size_t most = 0;
+  for (int i = 0; i < n_layers; ++i) {
+    const size_t b = mq_cache_attend_workspace_bytes(&at.caches[i], at.batch, at.q_heads,
+                                                     window_of(at, i));
+    most = b > most ? b : most;
+  }
+  return most;
+}
+
+// The layer loop of the stack entry points.  x == nullptr: h holds the
+// residual stream on entry; else h = x (bf16) first.  at: the attention, or
+// nullptr for the stack without.
+mq_status run_stack(const mq_layer* layers, int n_layers, const mq_stack_attention* at,
+                    const uint16_t* x, float* h, int64_t M, void* workspace,
+                    size_t workspace_bytes, hipStream_t st) {
   StackDims d;
   mq_status s = check_stack(layers, n_layers, M, &d);
   if (s != MQ_OK) return s;
@@ -472,6 +512,15 @@ mq_status run_stack(const mq_layer* layers, int n_layers, const uint16_t* x, flo
   if (!aligned16(h) || (x && !aligned16(x))) return MQ_ERR_ALIGN;
   size_t off[kStackBuffers], total;
   stack_offsets(d, M, off, &total);
+  const size_t att_off = total;
+  size_t scratch_off = 0, scratch = 0;
+  if (at) {
+    s = check_stack_attention(at, n_layers, d, M);
+    if (s != MQ_OK) return s;
+    scratch_off = att_off + up256((size_t)(M * d.H * 2));
+    scratch = stack_attention_scratch(*at, n_layers);
+    total = scratch_off + scratch;
+  }
   if (!workspace || workspace_bytes < total) return MQ_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return MQ_ERR_ALIGN;
   s = check_device();
@@ -487,6 +536,7 @@ mq_status run_stack(const mq_layer* layers, int n_layers, const uint16_t* x, flo
   float* dd = reinterpret_cast<float*>(ws + off[7]);
   uint16_t* qb = reinterpret_cast<uint16_t*>(ws + off[8]);
   uint16_t* ugb = reinterpret_cast<uint16_t*>(ws + off[9]);
+  uint16_t* att = at ? reinterpret_cast<uint16_t*>(ws + att_off) : nullptr;
 
   hipError_t e = x ? mq::launch_load_rmsnorm_bf16(x, h, a, M, d.H, st)
                    : mq::launch_rmsnorm_bf16(h, a, M, d.H, st);
@@ -502,7 +552,7 @@ mq_status run_stack(const mq_layer* layers, int n_layers, const uint16_t* x, flo
                                prob(L.v, L.r, a, nullptr, mq::kXBf16, v),
                                prob(L.up, L.r, a, nullptr, mq::kXBf16, u),
                                prob(L.gate, L.r, a, nullptr, mq::kXBf16, g)};
-    p1[0].ybf = qb;
+    p1[0].ybf = at ? nullptr : qb;
     if (pair) {
       p1[3].packed2 = L.gate.packed;
       p1[3].alpha2 = L.gate.alpha;
@@ -512,7 +562,15 @@ mq_status run_stack(const mq_layer* layers, int n_layers, const uint16_t* x, flo
     }
     s = run_mixed(p1, pair ? 4 : 5, M, st);
     if (s != MQ_OK) return s;
-    mq::SkinnyProblem p2[2] = {prob(L.o, L.r, qb, nullptr, mq::kXBf16, o),
+    if (at) {
+      s = mq_cache_append(&at->caches[i], at->batch, at->rope, k, v, d.Hkv, q, d.H, at->q_heads,
+                          MQ_F32, qb, st);
+      if (s != MQ_OK) return s;
+      s = mq_cache_attend(&at->caches[i], at->batch, qb, d.H, at->q_heads, at->scale, at->softcap,
+                          window_of(*at, i), 1, att, nullptr, ws + scratch_off, scratch, st);
+      if (s != MQ_OK) return s;
+    }
+    mq::SkinnyProblem p2[2] = {prob(L.o, L.r, at ? att : qb, nullptr, mq::kXBf16, o),
                                pair ? prob(L.down, L.r, ugb, nullptr, mq::kXBf16, dd)
                                     : prob(L.down, L.r, u, g, mq::kXF32Prod, dd)};
     // this launch (about a third of the layer's bytes, on fewer workgroups
@@ -540,14 +598,32 @@ mq_status mq_mixnmatch_forward(const mq_layer* layers, int n_layers, const uint1
                                int64_t M, float* h_out, void* workspace, size_t workspace_bytes,
                                void* stream) {
   if (!x) return MQ_ERR_NULL;
-  return run_stack(layers, n_layers, x, h_out, M, workspace, workspace_bytes,
+  return run_stack(layers, n_layers, nullptr, x, h_out, M, workspace, workspace_bytes,
                    (hipStream_t)stream);
 }
 
 mq_status mq_mixnmatch_forward_inplace(const mq_layer* layers, int n_layers, float* h,
                                        int64_t M, void* workspace, size_t workspace_bytes,
                                        void* stream) {
-  return run_stack(layers, n_layers, nullptr, h, M, workspace, workspace_bytes,
+  return run_stack(layers, n_layers, nullptr, nullptr, h, M, workspace, workspace_bytes,
+                   (hipStream_t)stream);
+}
+
+size_t mq_mixnmatch_attend_workspace_bytes(const mq_layer* layers, int n_layers,
+                                           const mq_stack_attention* attn, int64_t M) {
+  StackDims d;
+  if (check_stack(layers, n_layers, M, &d) != MQ_OK) return 0;
+  if (check_stack_attention(attn, n_layers, d, M) != MQ_OK) return 0;
+  size_t off[kStackBuffers], total;
+  stack_offsets(d, M, off, &total);
+  return total + up256((size_t)(M * d.H * 2)) + stack_attention_scratch(*attn, n_layers);
+}
+
+mq_status mq_mixnmatch_attend(const mq_layer* layers, int n_layers,
+                              const mq_stack_attention* attn, const uint16_t* x, int64_t M,
+                              float* h, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!attn) return MQ_ERR_NULL;
+  return run_stack(layers, n_layers, attn, x, h, M, workspace, workspace_bytes,
                    (hipStream_t)stream);
 }
 

@@ -94,6 +94,48 @@ mq::AttendArgs attend_args(const mq_kv_cache* c, const mq_kv_batch* b, int64_t q
 
 }  // namespace
 
+namespace mq {
+
+mq_status append_check(const mq_kv_cache* cache, const mq_kv_batch* batch,
+                       const mq_rope_spec* rope, const void* k, const void* v, int64_t kv_stride,
+                       const void* q, int64_t q_stride, int64_t q_heads, int x_type,
+                       const uint16_t* q_out) {
+  if (!k || !v || (q == nullptr) != (q_out == nullptr)) return MQ_ERR_NULL;
+  mq_status s = check_cache(cache);
+  if (s != MQ_OK) return s;
+  s = check_batch(batch, cache);
+  if (s != MQ_OK) return s;
+  if (x_type != MQ_BF16 && x_type != MQ_F32) return MQ_ERR_PRECISION;
+  const int64_t dim = cache->dim;
+  if (rope && (s = check_rope(rope, dim)) != MQ_OK) return s;
+  if (cache->heads > kMaxRowEntries / dim) return MQ_ERR_SHAPE;
+  if ((s = check_strided(k, kv_stride, cache->heads * dim)) != MQ_OK) return s;
+  if ((s = check_strided(v, kv_stride, cache->heads * dim)) != MQ_OK) return s;
+  if (q) {
+    if (q_heads < 1 || q_heads > kMaxRowEntries / dim) return MQ_ERR_SHAPE;
+    if ((s = check_strided(q, q_stride, q_heads * dim)) != MQ_OK) return s;
+    if (misaligned(q_out, 16)) return MQ_ERR_ALIGN;
+  }
+  return MQ_OK;
+}
+
+mq_status attend_check(const mq_kv_cache* cache, const mq_kv_batch* batch, const uint16_t* q,
+                       int64_t q_stride, int64_t q_heads, float scale, float softcap,
+                       int64_t window, int causal, const uint16_t* out, const float* lse) {
+  if (!q || !out) return MQ_ERR_NULL;
+  mq_status s = check_attend(cache, batch, q_heads, window);
+  if (s != MQ_OK) return s;
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f ||
+      (softcap > 0.f && softcap < 1e-30f) || (causal != 0 && causal != 1))
+    return MQ_ERR_PRECISION;
+  if (window > 0 && !causal) return MQ_ERR_SHAPE;
+  if ((s = check_strided(q, q_stride, q_heads * cache->dim)) != MQ_OK) return s;
+  if (misaligned(out, 16) || misaligned(lse, 4)) return MQ_ERR_ALIGN;
+  return MQ_OK;
+}
+
+}  // namespace mq
+
 extern "C" {
 
 mq_status mq_rope(const mq_rope_spec* rope, const int32_t* positions, const void* x, int x_type,
@@ -120,22 +162,9 @@ mq_status mq_cache_append(const mq_kv_cache* cache, const mq_kv_batch* batch,
                           const mq_rope_spec* rope, const void* k, const void* v,
                           int64_t kv_stride, const void* q, int64_t q_stride, int64_t q_heads,
                           int x_type, uint16_t* q_out, void* stream) {
-  if (!k || !v || (q == nullptr) != (q_out == nullptr)) return MQ_ERR_NULL;
-  mq_status s = check_cache(cache);
+  mq_status s = mq::append_check(cache, batch, rope, k, v, kv_stride, q, q_stride, q_heads, x_type,
+                                 q_out);
   if (s != MQ_OK) return s;
-  s = check_batch(batch, cache);
-  if (s != MQ_OK) return s;
-  if (x_type != MQ_BF16 && x_type != MQ_F32) return MQ_ERR_PRECISION;
-  const int64_t dim = cache->dim;
-  if (rope && (s = check_rope(rope, dim)) != MQ_OK) return s;
-  if (cache->heads > kMaxRowEntries / dim) return MQ_ERR_SHAPE;
-  if ((s = check_strided(k, kv_stride, cache->heads * dim)) != MQ_OK) return s;
-  if ((s = check_strided(v, kv_stride, cache->heads * dim)) != MQ_OK) return s;
-  if (q) {
-    if (q_heads < 1 || q_heads > kMaxRowEntries / dim) return MQ_ERR_SHAPE;
-    if ((s = check_strided(q, q_stride, q_heads * dim)) != MQ_OK) return s;
-    if (misaligned(q_out, 16)) return MQ_ERR_ALIGN;
-  }
   s = mq::device_check();
   if (s != MQ_OK) return s;
   return done(mq::launch_cache_append(cache_of(cache), batch_of(batch), rope_of(rope), k, v,
@@ -169,15 +198,9 @@ mq_status mq_cache_attend(const mq_kv_cache* cache, const mq_kv_batch* batch, co
                           int64_t q_stride, int64_t q_heads, float scale, float softcap,
                           int64_t window, int causal, uint16_t* out, float* lse, void* workspace,
                           size_t workspace_bytes, void* stream) {
-  if (!q || !out) return MQ_ERR_NULL;
-  mq_status s = check_attend(cache, batch, q_heads, window);
+  mq_status s = mq::attend_check(cache, batch, q, q_stride, q_heads, scale, softcap, window, causal,
+                                 out, lse);
   if (s != MQ_OK) return s;
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f ||
-      (softcap > 0.f && softcap < 1e-30f) || (causal != 0 && causal != 1))
-    return MQ_ERR_PRECISION;
-  if (window > 0 && !causal) return MQ_ERR_SHAPE;
-  if ((s = check_strided(q, q_stride, q_heads * cache->dim)) != MQ_OK) return s;
-  if (misaligned(out, 16) || misaligned(lse, 4)) return MQ_ERR_ALIGN;
   mq::AttendArgs a = attend_args(cache, batch, q_heads, window);
   const size_t need = mq::attend_plan(a);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MQ_ERR_WORKSPACE;

@@ -178,6 +178,14 @@ hipError_t launch_cache_read(const KvCache& c, const KvBatch& b, void* k_out, vo
 // Bytes of partial results; fills piece and pieces.
 size_t attend_plan(AttendArgs& a);
 hipError_t launch_attend(AttendArgs& a, hipStream_t s);
+// Argument checks of mq_cache_append and mq_cache_attend (device and workspace
+// left out), for calls made from inside the library.
+mq_status append_check(const mq_kv_cache* c, const mq_kv_batch* b, const mq_rope_spec* rope,
+                       const void* k, const void* v, int64_t kv_stride, const void* q,
+                       int64_t q_stride, int64_t q_heads, int x_type, const uint16_t* q_out);
+mq_status attend_check(const mq_kv_cache* c, const mq_kv_batch* b, const uint16_t* q,
+                       int64_t q_stride, int64_t q_heads, float scale, float softcap,
+                       int64_t window, int causal, const uint16_t* out, const float* lse);
 // MQ_OK if the current device is a gfx950.
 mq_status device_check();
 
