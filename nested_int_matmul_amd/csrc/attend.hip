@@ -68,6 +68,16 @@ __device__ __forceinline__ void codes_to_f16(u32x4 w, f16x8* a, f16x8* b) {
   *b = r.v[1];
 }
 
+// tanh(z) = 1 - 2 / (e^2z + 1), by its series where that cancels (cut below
+// 2^-29 of it).
+__device__ __forceinline__ float capped(float z) {
+  const float e2 = __builtin_amdgcn_exp2f(2.f * kLog2e * fabsf(z));
+  const float big = copysignf(1.f - 2.f / (e2 + 1.f), z);
+  const float zz = z * z;
+  const float small = z * (1.f + zz * (-1.f / 3.f + zz * (2.f / 15.f + zz * (-17.f / 315.f))));
+  return fabsf(z) < 0.125f ? small : big;
+}
+
 // Keys [lo, hi) of the token at position pos.
 struct Keys {
   int64_t lo, hi;
@@ -278,14 +288,7 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
         for (int i = 0; i < 4; ++i) {
           float y = sc[rt][t][i] * f;
           if (CAP) {
-            // tanh(z) = 1 - 2 / (e^2z + 1), by its series where that cancels
-            const float z = y / a.softcap;
-            const float e2 = __builtin_amdgcn_exp2f(2.f * kLog2e * fabsf(z));
-            const float big = copysignf(1.f - 2.f / (e2 + 1.f), z);
-            const float zz = z * z;
-            const float small =
-                z * (1.f + zz * (-1.f / 3.f + zz * (2.f / 15.f + zz * (-17.f / 315.f))));
-            y = (fabsf(z) < 0.125f ? small : big) * (a.softcap * kLog2e);
+            y = capped(y / a.softcap) * (a.softcap * kLog2e);
           }
           x[4 * t + i] = y;
         }
@@ -404,6 +407,328 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
   }
 }
 
+// ------------------------------------------------------------ many rows
+//
+// NW waves of 32 rows each (32x32x16 products), one 64-key tile after the
+// other for all of them.  The tile's codes are converted to fp16 once for the
+// workgroup and staged through LDS as operand fragments (two buffers, one
+// barrier a tile); a lane's fragment is 16 consecutive bytes, and fragments
+// are permuted within groups of eight lanes (an XOR with the fragment's
+// index) so that both the staging stores and the operand loads touch all
+// banks evenly.  The 32 key rows of an S^T product are ordered so that a lane
+// (row lane % 32, half h = lane / 32) gets keys 16 e + 8 h + 0..7 of the tile
+// in registers 8 e .. 8 e + 7: eight consecutive keys of one 16-key group, the
+// operand of the second product as it stands.  A 16-key group lies in one
+// page, so its scales are the same for all lanes.
+//
+// The v scale of a group goes into the exponent: p = exp2(t - ref + log2 w),
+// w = v_scale / (largest v_scale so far), which saves a multiplication a
+// probability; the row's sum takes (sum of the group's p) / w.
+template <int DIM, int NW, bool E4M3, bool CAP>
+__global__ void __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(DIM == 256 ? 1 : 2)))
+attend_many_kernel(AttendArgs a) {
+  constexpr int T = NW * 64;      // threads
+  constexpr int KS = DIM / 16;    // 16-dim steps of the first product
+  constexpr int DT = DIM / 32;    // 32-dim tiles of the output
+  constexpr int KC = 64 * KS / T; // 16-code pieces of k (and of v) a thread
+  static_assert(64 * KS % T == 0, "pieces");
+  __shared__ u32x4 lds_k[2][2][KS][64];
+  __shared__ u32x4 lds_v[2][4][DT][64];
+  __shared__ float lds_ks[2][4], lds_vs[2][4];
+  __shared__ int lds_live[2][4];
+
+  const int s = blockIdx.z;
+  const int kvh = blockIdx.x % a.cache.heads;
+  const SeqSpan sp = seq_span(a.batch, s);
+  const int rows = sp.n * a.group;
+  const int tiles = (rows + NW * 32 - 1) / (NW * 32);
+  // last rows first: with a causal mask they see the most keys
+  const int row_tile = tiles - 1 - (int)(blockIdx.x / a.cache.heads);
+  if (row_tile < 0) return;
+  const int row_base = row_tile * (NW * 32);
+  const int row_last = row_base + NW * 32 < rows ? row_base + NW * 32 - 1 : rows - 1;
+  const int64_t held = held_of(a, s);
+  const Span span = span_of(a, sp, held, row_base / a.group, row_last / a.group);
+  const int piece = blockIdx.y;
+  if (piece > 0 && piece >= span.pieces) return;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, r32 = lane & 31;
+
+  // ---- this lane's row
+  const int row = row_base + wave * 32 + r32;
+  const bool real = row < rows;
+  const int tok = real ? row / a.group : 0;
+  const int head = kvh * a.group + (real ? row - tok * a.group : 0);
+  f16x8 q[KS];
+  float qf;
+  {
+    const uint16_t* qp = a.q + (int64_t)(sp.row0 + tok) * a.q_stride + (int64_t)head * DIM + 8 * h;
+    u32x4 raw[KS];
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      raw[k] = real ? *reinterpret_cast<const u32x4*>(qp + 16 * k) : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t x = raw[k][e] & 0x7fffu, y = (raw[k][e] >> 16) & 0x7fffu;
+        top = x > top ? x : top;
+        top = y > top ? y : top;
+      }
+    }
+    const uint32_t o = __shfl_xor(top, 32);
+    top = o > top ? o : top;
+    int e = (int)(top >> 7) - 127;
+    e = e < -100 ? -100 : (e > 127 ? 14 : e);
+    // (a negative scale turns the queries round, so that factors are >= 0)
+    const float up = copysignf(__uint_as_float((uint32_t)(14 - e + 127) << 23), a.scale);
+    qf = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * fabsf(a.scale);
+    if (!CAP) qf *= kLog2e;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t pair = raw[k][j >> 1];
+        const float x = __uint_as_float((j & 1) ? pair & 0xffff0000u : pair << 16);
+        q[k][j] = (_Float16)(x * up);
+      }
+  }
+  const Keys see = keys_of(a, sp.start + tok, held);
+  // keys that some, and that all, of this wave's rows see
+  const int wrow = row_base + wave * 32;
+  const int wlast = wrow + 31 < rows ? wrow + 31 : rows - 1;
+  const bool wreal = wrow < rows;
+  const Keys wf = keys_of(a, sp.start + (wreal ? wrow / a.group : 0), held);
+  const Keys wl = keys_of(a, sp.start + (wreal ? wlast / a.group : 0), held);
+
+  const int64_t begin = span.lo + (int64_t)piece * a.piece;
+  const int64_t stop = begin + a.piece < span.hi ? begin + a.piece : span.hi;
+  const int block = a.cache.block, shift = __builtin_ctz(block);
+  const int64_t page_bytes = (int64_t)block * DIM;
+
+  f32x16 acc[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) acc[d] = f32x16{};
+  float ref = kNoRef, sum = 0.f, vref = 0.f;
+
+  // ---- staging: pages one tile further ahead than codes
+  u32x4 kc[KC], vc[KC];
+  float ksc[KC] = {}, vsc = 0.f;
+  int pk[KC], pv[KC], live0 = 0;
+  auto load_pages = [&](int64_t key0) {
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+      const int c = tid + i * T;
+      const int64_t kk = key0 + (c / KS & ~15), kv = key0 + (c & 3) * 16;
+      pk[i] = kk < stop ? page_of(a.batch, s, kk >> shift, a.cache.pages) : -1;
+      pv[i] = kv < stop ? page_of(a.batch, s, kv >> shift, a.cache.pages) : -1;
+    }
+  };
+  auto load_codes = [&](int64_t key0) {
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+      const int c = tid + i * T;
+      const int key = c / KS, ks = c % KS, dim = c >> 2, kst = c & 3;
+      const int64_t hk = (int64_t)(pk[i] < 0 ? 0 : pk[i]) * a.cache.heads + kvh;
+      const int64_t hv = (int64_t)(pv[i] < 0 ? 0 : pv[i]) * a.cache.heads + kvh;
+      kc[i] = *reinterpret_cast<const u32x4*>(
+          a.cache.k + hk * page_bytes + (int64_t)((key0 + key) & (block - 1)) * DIM + 16 * ks);
+      vc[i] = *reinterpret_cast<const u32x4*>(a.cache.v + hv * page_bytes + (int64_t)dim * block +
+                                              ((key0 + 16 * kst) & (block - 1)));
+      const int64_t n = stop - (key0 + 16 * kst);
+      const int live = pv[i] < 0 || n <= 0 ? 0 : (n < 16 ? (int)n : 16);
+      if (live < 16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int keep = live - 4 * e;
+          vc[i][e] &= keep >= 4 ? 0xffffffffu : (keep <= 0 ? 0u : (1u << (8 * keep)) - 1);
+        }
+      }
+      if (i == 0) live0 = live;
+      if (ks == 0 && (key & 15) == 0) ksc[i] = a.cache.k_scale[hk];
+      if (i == 0 && dim == 0) vsc = a.cache.v_scale[hv];
+    }
+  };
+  auto store_tile = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+      const int c = tid + i * T;
+      const int key = c / KS, ks = c % KS, dim = c >> 2, kst = c & 3;
+      f16x8 lo, hi;
+      codes_to_f16<E4M3>(kc[i], &lo, &hi);
+      // row of the S^T product that gives this key: see above
+      const int e = key & 15, m = (key & 16) | ((e & 8) >> 1) | ((e & 4) << 1) | (e & 3);
+      const int swk = KS == 4 ? 2 * ks : ks & 7;
+      lds_k[buf][key >> 5][ks][m ^ swk] = __builtin_bit_cast(u32x4, lo);
+      lds_k[buf][key >> 5][ks][(32 + m) ^ swk] = __builtin_bit_cast(u32x4, hi);
+      codes_to_f16<E4M3>(vc[i], &lo, &hi);
+      const int swv = 2 * kst;
+      lds_v[buf][kst][dim >> 5][(dim & 31) ^ swv] = __builtin_bit_cast(u32x4, lo);
+      lds_v[buf][kst][dim >> 5][(32 + (dim & 31)) ^ swv] = __builtin_bit_cast(u32x4, hi);
+      if (ks == 0 && (key & 15) == 0) lds_ks[buf][key >> 4] = ksc[i];
+      if (i == 0 && dim == 0) {
+        lds_vs[buf][kst] = live0 > 0 ? vsc : 0.f;
+        lds_live[buf][kst] = live0;
+      }
+    }
+  };
+
+  if (begin < stop) {
+    load_pages(begin);
+    load_codes(begin);
+    load_pages(begin + 64);
+    store_tile(0);
+    load_codes(begin + 64);
+    load_pages(begin + 128);
+  }
+  int buf = 0;
+  for (int64_t key0 = begin; key0 < stop; key0 += 64, buf ^= 1) {
+    __syncthreads();
+    if (key0 + 64 < stop) {
+      store_tile(buf ^ 1);
+      load_codes(key0 + 128);
+      load_pages(key0 + 192);
+    }
+    if (!wreal || key0 >= wl.hi || key0 + 64 <= wf.lo) continue;
+
+    // ---- S^T
+    f32x16 sc[2];
+    sc[0] = f32x16{};
+    sc[1] = f32x16{};
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const int sw = KS == 4 ? 2 * k : k & 7;
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+        sc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            __builtin_bit_cast(f16x8, lds_k[buf][kt][k][lane ^ sw]), q[k], sc[kt], 0, 0, 0);
+    }
+    float f[4], w[4];
+    float vtop = 0.f;
+    bool full = true;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // (not 0, so that it keeps a masked key's -infinity: a page of zeros)
+      f[e] = fmaxf(lds_ks[buf][e] * qf, 0x1p-120f);
+      w[e] = lds_vs[buf][e];
+      vtop = fmaxf(vtop, w[e]);
+      full = full && lds_live[buf][e] == 16;
+    }
+    if (vtop > vref) {  // the same in all lanes
+      const float g = vref / vtop;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) acc[d] = acc[d] * g;
+      vref = vtop;
+    }
+    const float vinv = vref > 0.f ? 1.f / vref : 0.f;
+    // (a page of zeros, or one 2^-60 below another, adds nothing to the
+    // output: its w only has to cancel in the sum)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = fmaxf(w[e] * vinv, 0x1p-60f);
+
+    if (CAP) {
+      const float ci = 1.f / a.softcap;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float z = sc[e >> 1][8 * (e & 1) + i] * (f[e] * ci);
+          sc[e >> 1][8 * (e & 1) + i] = capped(z) * (a.softcap * kLog2e);
+        }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = 1.f;
+    }
+    if (!full || key0 < wl.lo || key0 + 64 > wf.hi) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int live = lds_live[buf][e];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t j = key0 + 16 * e + 8 * h + i;
+          if (8 * h + i >= live || j < see.lo || j >= see.hi)
+            sc[e >> 1][8 * (e & 1) + i] = -INFINITY;
+        }
+      }
+    }
+    // ---- reference
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float m = sc[e >> 1][8 * (e & 1)];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = fmaxf(m, sc[e >> 1][8 * (e & 1) + i]);
+      top = fmaxf(top, m * f[e]);
+    }
+    if (__any(top > ref + kSlack)) {
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float m = fmaxf(top, ref);
+      const float g = __builtin_amdgcn_exp2f(ref - m);
+      ref = m;
+      sum *= g;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) acc[d] = acc[d] * g;
+    }
+    // ---- probabilities
+    f16x8 p[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float c = __builtin_amdgcn_logf(w[e]) - ref;
+      float part = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(sc[e >> 1][8 * (e & 1) + i], f[e], c));
+        const float y = __builtin_amdgcn_exp2f(fmaf(sc[e >> 1][8 * (e & 1) + i + 1], f[e], c));
+        part += x + y;
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        const f16x2 xy = __builtin_convertvector(f32x2{x, y}, f16x2);
+        p[e][i] = xy[0];
+        p[e][i + 1] = xy[1];
+      }
+      sum = fmaf(part, 1.f / w[e], sum);
+    }
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            __builtin_bit_cast(f16x8, lds_v[buf][e][d][lane ^ (2 * e)]), p[e], acc[d], 0, 0, 0);
+  }
+
+  sum += __shfl_xor(sum, 32);
+  if (!real) return;
+  const int64_t out_row = (int64_t)(sp.row0 + tok) * a.q_heads + head;
+  if (span.pieces <= 1) {
+    const float inv = sum == 0.f ? 0.f : vref / sum;
+    uint16_t* o = a.out + out_row * DIM + 4 * h;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        u32x2 b;
+        b[0] = bf16_rne(acc[d][4 * i] * inv) | (bf16_rne(acc[d][4 * i + 1] * inv) << 16);
+        b[1] = bf16_rne(acc[d][4 * i + 2] * inv) | (bf16_rne(acc[d][4 * i + 3] * inv) << 16);
+        if (sum == 0.f) b = u32x2{0, 0};
+        *reinterpret_cast<u32x2*>(o + 32 * d + 8 * i) = b;
+      }
+    if (a.lse && h == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+  } else {
+    const int64_t at = (int64_t)piece * a.batch.rows * a.q_heads + out_row;
+    float* o = a.part_o + at * DIM + 4 * h;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x4*>(o + 32 * d + 8 * i) =
+            f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]} * vref;
+    if (h == 0) {
+      a.part_ml[2 * at] = ref;
+      a.part_ml[2 * at + 1] = sum;
+    }
+  }
+}
+
 // ------------------------------------------------------------- the join
 //
 // One wave a row: the pieces' references and sums, then their outputs.
@@ -449,7 +774,12 @@ __global__ void __launch_bounds__(256) join_kernel(AttendArgs a, int tile_rows) 
 namespace {
 
 // Rows of a workgroup for max_new tokens of `group` heads each.
-int rows_tile(int64_t most_rows) { return most_rows <= 16 ? 16 : 32; }
+// Up to 32 rows share the codes' way through one wave's registers; more are
+// worth converting the codes once for all of them.
+constexpr int many_waves(int dim) { return dim == 128 ? 8 : 4; }
+int rows_tile(int64_t most_rows, int dim) {
+  return most_rows <= 16 ? 16 : most_rows <= 32 ? 32 : many_waves(dim) * 32;
+}
 constexpr int kFewWaves = 4;
 
 template <int DIM, int ROWS, int NW>
@@ -471,12 +801,33 @@ hipError_t few(const AttendArgs& a, dim3 grid, hipStream_t s) {
 }
 
 template <int DIM>
+hipError_t many(const AttendArgs& a, dim3 grid, hipStream_t s) {
+  constexpr int NW = many_waves(DIM);
+  const dim3 block(NW * 64);
+  const bool cap = a.softcap > 0.f;
+  if (a.cache.e4m3) {
+    if (cap)
+      hipLaunchKernelGGL((attend_many_kernel<DIM, NW, true, true>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((attend_many_kernel<DIM, NW, true, false>), grid, block, 0, s, a);
+  } else {
+    if (cap)
+      hipLaunchKernelGGL((attend_many_kernel<DIM, NW, false, true>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((attend_many_kernel<DIM, NW, false, false>), grid, block, 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+template <int DIM>
 hipError_t attend_dim(AttendArgs& a, hipStream_t s) {
   const int64_t most = (int64_t)a.batch.max_new * a.group;
-  const int tile = rows_tile(most);
+  const int tile = rows_tile(most, a.cache.dim);
   const dim3 grid((unsigned)(a.cache.heads * ((most + tile - 1) / tile)), (unsigned)a.pieces,
                   (unsigned)a.batch.seqs);
-  hipError_t e = tile == 16 ? few<DIM, 1, kFewWaves>(a, grid, s) : few<DIM, 2, kFewWaves>(a, grid, s);
+  hipError_t e = tile == 16   ? few<DIM, 1, kFewWaves>(a, grid, s)
+                 : tile == 32 ? few<DIM, 2, kFewWaves>(a, grid, s)
+                              : many<DIM>(a, grid, s);
   if (e != hipSuccess || a.pieces <= 1) return e;
   const dim3 jg((unsigned)((most + 3) / 4), (unsigned)a.cache.heads, (unsigned)a.batch.seqs);
   hipLaunchKernelGGL((join_kernel<DIM>), jg, dim3(256), 0, s, a, tile);
@@ -487,7 +838,7 @@ hipError_t attend_dim(AttendArgs& a, hipStream_t s) {
 
 size_t attend_plan(AttendArgs& a) {
   const int64_t most = (int64_t)a.batch.max_new * a.group;
-  const int tile = rows_tile(most);
+  const int tile = rows_tile(most, a.cache.dim);
   int64_t keys = (int64_t)a.batch.table_pages * a.cache.block;
   if (a.window > 0 && a.window + a.batch.max_new + 64 < keys)
     keys = a.window + a.batch.max_new + 64;
