@@ -10,12 +10,13 @@ constexpr int kThreads = 256;
 // ------------------------------------------------------------------ mq_rope
 //
 // A thread owns one unit (eight entries, four pairs) of one token and walks
-// over `per` heads, so the four float64 sines and cosines (about 45
-// instructions a pair) are found once for all of them; their angles do not
-// depend on the head.  Lanes of a wave hold consecutive units: 8 or 16 bytes
-// each, whole lines together.
+// over `per` heads, four at a time in flight, so the four float64 sines and
+// cosines (about 45 instructions a pair) are found once for all of them; the
+// angles do not depend on the head.  Lanes of a wave hold consecutive units:
+// 8 or 16 bytes each, whole lines together.
+template <bool F32>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeSpec r, const int* positions,
-                                                        const void* x, bool f32, int64_t x_stride,
+                                                        const void* x, int64_t x_stride,
                                                         int64_t rows, int heads, int dim,
                                                         uint16_t* out, int64_t out_stride,
                                                         int per) {
@@ -25,26 +26,26 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeSpec r, const int* p
   const int64_t row = (int64_t)blockIdx.x * slots + slot;
   if (slot >= slots || row >= rows) return;
   const Unit un = unit_of(u, r.rot, r.interleaved);
-  double c[4], s[4];
-  if (un.turns) {
-    const double pos = (double)positions[row];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sincos64(pos * r.freq[un.pair0 + i], &s[i], &c[i]);
-      s[i] *= r.factor;
-      c[i] *= r.factor;
-    }
-  }
   const int h0 = blockIdx.y * per, h1 = h0 + per < heads ? h0 + per : heads;
-  for (int h = h0; h < h1; ++h) {
-    float v[8];
-    load_unit(x, f32, row * x_stride + (int64_t)h * dim, un, v);
-    if (un.turns) turn_unit(v, c, s, r.interleaved);
-    uint32_t w[4];
-    pack_unit(v, w);
-    uint16_t* o = out + row * out_stride + (int64_t)h * dim;
-    *reinterpret_cast<u32x2*>(o + un.lo) = u32x2{w[0], w[1]};
-    *reinterpret_cast<u32x2*>(o + un.hi) = u32x2{w[2], w[3]};
+  Turn turn;
+  RawUnit<F32> raw[4];
+  for (int h = h0; h < h1; h += 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (h + j < h1) raw[j] = load_unit<F32>(x, row * x_stride + (int64_t)(h + j) * dim, un);
+    if (h == h0 && un.turns) turn.at(r, un, (double)positions[row], r.factor);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (h + j >= h1) continue;
+      float v[8];
+      numbers_of_unit<F32>(raw[j], v);
+      if (un.turns) turn_unit(v, turn.c, turn.s, r.interleaved);
+      uint32_t w[4];
+      pack_unit(v, w);
+      uint16_t* o = out + row * out_stride + (int64_t)(h + j) * dim;
+      *reinterpret_cast<u32x2*>(o + un.lo) = u32x2{w[0], w[1]};
+      *reinterpret_cast<u32x2*>(o + un.hi) = u32x2{w[2], w[3]};
+    }
   }
 }
 
@@ -54,13 +55,17 @@ hipError_t launch_rope(const RopeSpec& r, const int* positions, const void* x, b
   if (rows == 0) return hipSuccess;
   const int slots = kThreads / (dim / 8);
   const int64_t groups = (rows + slots - 1) / slots;
-  // heads of a thread: as many as leave 2048 workgroups (eight a CU)
-  int per = 16;
-  while (per > 1 && groups * ((heads + per - 1) / per) < 2048) per >>= 1;
+  // heads of a thread: as many as leave 512 workgroups (two a CU)
+  int per = 8;
+  while (per > 1 && groups * ((heads + per - 1) / per) < 512) per >>= 1;
   while ((heads + per - 1) / per > 65535) per <<= 1;
   const dim3 grid((unsigned)groups, (unsigned)((heads + per - 1) / per));
-  hipLaunchKernelGGL(rope_kernel, grid, dim3(kThreads), 0, s, r, positions, x, f32, x_stride,
-                     rows, heads, dim, out, out_stride, per);
+  if (f32)
+    hipLaunchKernelGGL(rope_kernel<true>, grid, dim3(kThreads), 0, s, r, positions, x, x_stride,
+                       rows, heads, dim, out, out_stride, per);
+  else
+    hipLaunchKernelGGL(rope_kernel<false>, grid, dim3(kThreads), 0, s, r, positions, x, x_stride,
+                       rows, heads, dim, out, out_stride, per);
   return hipGetLastError();
 }
 
@@ -69,55 +74,63 @@ hipError_t launch_rope(const RopeSpec& r, const int* positions, const void* x, b
 // One workgroup per (sequence, page that gets tokens, head, k or v): the
 // page's new values stay in registers as bf16 (at most 64 dwords a thread)
 // between finding the scale and rounding to codes, so they are read once, and
-// no other workgroup touches the page's scale or codes.  A thread owns one
-// unit of every (256 / units)-th token; k's angles of a thread advance by a
-// constant step, so its sines and cosines follow by one complex product a
-// token in float64 (error below 2^-48 over a page) in place of an evaluation.
-// v is held dim-major: pages that get 16 tokens or more go through LDS and
-// leave in 16-byte pieces, fewer tokens go out as single bytes.
+// no other workgroup touches the page's scale or codes.  Eight tokens' loads
+// (four of fp32) are in flight before the first is used.  k's angles of a
+// thread advance by a constant step, so its sines and cosines follow by one
+// complex product a token in place of an evaluation.
+// v is held dim-major: pages that get 16 tokens or more go through LDS, four
+// tokens of a dim to a dword, and leave in 16-byte pieces; fewer tokens go out
+// as single bytes.
 //
 // The queries' workgroups (blockIdx.y >= 2 * heads) take eight tokens of the
 // same page each, all heads.
 
-// eight tokens of one page, all query heads
-template <int DIM>
-__device__ __forceinline__ void append_queries(const KvBatch& b, const RopeSpec& r,
-                                               const SeqSpan& sp, int64_t lo, int64_t hi,
-                                               const void* q, int64_t q_stride, int q_heads,
-                                               bool f32, uint16_t* q_out) {
+constexpr int kQueryTokens = 8;
+
+// at most eight tokens of one page, all query heads
+template <int DIM, bool F32>
+__device__ __forceinline__ void append_queries(const RopeSpec& r, const SeqSpan& sp, int64_t lo,
+                                               int64_t hi, const void* q, int64_t q_stride,
+                                               int q_heads, uint16_t* q_out) {
   constexpr int U = DIM / 8, SLOTS = kThreads / U;
   const int u = threadIdx.x % U, slot = threadIdx.x / U;
   const int hs = q_heads < SLOTS ? q_heads : SLOTS;  // heads side by side
   const int toks = SLOTS / hs;                       // tokens side by side
   const int head0 = slot % hs, tok0 = slot / hs;
   if (tok0 >= toks) return;
-  const Unit un = unit_of(u, r.rot, r.interleaved);
-  const bool turns = r.freq && un.turns;
+  const Unit un = unit_of(u, r.freq ? r.rot : 0, r.interleaved);
+  Turn turn, step;
   for (int64_t pos = lo + tok0; pos < hi; pos += toks) {
-    double c[4], s[4];
-    if (turns) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sincos64((double)pos * r.freq[un.pair0 + i], &s[i], &c[i]);
-        s[i] *= r.factor;
-        c[i] *= r.factor;
-      }
-    }
     const int64_t row = sp.row0 + (pos - sp.start);
-    for (int h = head0; h < q_heads; h += hs) {
-      float v[8];
-      load_unit(q, f32, row * q_stride + (int64_t)h * DIM, un, v);
-      if (turns) turn_unit(v, c, s, r.interleaved);
-      uint32_t w[4];
-      pack_unit(v, w);
-      uint16_t* o = q_out + (row * q_heads + h) * DIM;
-      *reinterpret_cast<u32x2*>(o + un.lo) = u32x2{w[0], w[1]};
-      *reinterpret_cast<u32x2*>(o + un.hi) = u32x2{w[2], w[3]};
+    for (int h = head0; h < q_heads; h += 4 * hs) {
+      RawUnit<F32> raw[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (h + j * hs < q_heads)
+          raw[j] = load_unit<F32>(q, row * q_stride + (int64_t)(h + j * hs) * DIM, un);
+      if (h == head0 && un.turns) {
+        if (pos == lo + tok0) {
+          turn.at(r, un, (double)pos, r.factor);
+          if (pos + toks < hi) step.at(r, un, (double)toks, 1.0);
+        } else {
+          turn.advance(step);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (h + j * hs >= q_heads) continue;
+        float v[8];
+        numbers_of_unit<F32>(raw[j], v);
+        if (un.turns) turn_unit(v, turn.c, turn.s, r.interleaved);
+        uint32_t w[4];
+        pack_unit(v, w);
+        uint16_t* o = q_out + (row * q_heads + h + j * hs) * DIM;
+        *reinterpret_cast<u32x2*>(o + un.lo) = u32x2{w[0], w[1]};
+        *reinterpret_cast<u32x2*>(o + un.hi) = u32x2{w[2], w[3]};
+      }
     }
   }
 }
-
-constexpr int kQueryTokens = 8;
 
 // a bf16 pattern's value as a quotient's dividend, and whether it is a number
 __device__ __forceinline__ float code_quotient(uint32_t bits, float s, float rs) {
@@ -127,15 +140,17 @@ __device__ __forceinline__ float code_quotient(uint32_t bits, float s, float rs)
   return exact_quotient(__uint_as_float(bits << 16), s, rs);
 }
 
-template <int DIM, int BLOCK>
+template <int DIM, int BLOCK, bool F32>
 __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch b, RopeSpec r,
                                                           const void* k, const void* v,
                                                           int64_t kv_stride, const void* q,
-                                                          int64_t q_stride, int q_heads, bool f32,
+                                                          int64_t q_stride, int q_heads,
                                                           uint16_t* q_out) {
   constexpr int U = DIM / 8, SLOTS = kThreads / U;
   constexpr int STEPS = BLOCK / SLOTS > 0 ? BLOCK / SLOTS : 1;
-  constexpr int PITCH = BLOCK + 4;  // bytes of a dim's row in LDS
+  constexpr int ONCE = F32 ? 4 : 8;            // steps loaded before the first is used
+  constexpr int G = STEPS < 4 ? STEPS : 4;     // consecutive tokens a thread has of v
+  constexpr int PITCH = BLOCK + 4;             // bytes of a dim's row in LDS
   __shared__ uint32_t tile[DIM * PITCH / 4];
   __shared__ uint32_t wave_max[kThreads / 64];
 
@@ -154,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch
     lo = lo > base + part * kQueryTokens ? lo : base + part * kQueryTokens;
     const int64_t last = base + (part + 1) * kQueryTokens;
     hi = hi < last ? hi : last;
-    if (lo < hi) append_queries<DIM>(b, r, sp, lo, hi, q, q_stride, q_heads, f32, q_out);
+    if (lo < hi) append_queries<DIM, F32>(r, sp, lo, hi, q, q_stride, q_heads, q_out);
     return;
   }
   const int page = page_of(b, seq, pi, cache.pages);
@@ -172,42 +187,50 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch
 
   // ---- the page's new values as bf16, and their largest magnitude
   const Unit un = is_v ? unit_of(u, 0, false) : unit_of(u, r.freq ? r.rot : 0, r.interleaved);
+  // place in the page of this thread's j-th token
+  auto place = [&](int j) {
+    return is_v ? (j / G) * (G * SLOTS) + slot * G + j % G : slot + j * SLOTS;
+  };
+  const void* src = is_v ? v : k;
+  const int64_t at0 = (sp.row0 + (base - sp.start)) * kv_stride + (int64_t)head * DIM;
   uint32_t w[STEPS][4];
   uint32_t top = 0;
-  double c[4], s[4], dc[4], ds[4];
-  if (un.turns) {
+  Turn turn, step;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const double f = r.freq[un.pair0 + i];
-      sincos64((double)(base + slot) * f, &s[i], &c[i]);
-      s[i] *= r.factor;
-      c[i] *= r.factor;
-      if (STEPS > 1) sincos64((double)SLOTS * f, &ds[i], &dc[i]);
+  for (int j0 = 0; j0 < STEPS; j0 += ONCE) {
+    RawUnit<F32> raw[ONCE];
+#pragma unroll
+    for (int j = j0; j < j0 + ONCE && j < STEPS; ++j) {
+      const int t = place(j);
+      if (t >= used && t < fill) raw[j - j0] = load_unit<F32>(src, at0 + t * kv_stride, un);
     }
-  }
-#pragma unroll
-  for (int j = 0; j < STEPS; ++j) {
-    const int t = slot + j * SLOTS;
-    if (t >= used && t < fill) {
-      float x[8];
-      const int64_t row = sp.row0 + (base + t - sp.start);
-      load_unit(is_v ? v : k, f32, row * kv_stride + (int64_t)head * DIM, un, x);
-      if (un.turns) turn_unit(x, c, s, r.interleaved);
-      pack_unit(x, w[j]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a = w[j][i] & 0x7fffu, d = (w[j][i] >> 16) & 0x7fffu;
-        top = a < 0x7f80u && a > top ? a : top;
-        top = d < 0x7f80u && d > top ? d : top;
-      }
+    if (j0 == 0 && un.turns) {
+      turn.at(r, un, (double)(base + slot), r.factor);
+      if (STEPS > 1) step.at(r, un, (double)SLOTS, 1.0);
     }
-    if (un.turns && j + 1 < STEPS) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const double nc = c[i] * dc[i] - s[i] * ds[i];
-        s[i] = s[i] * dc[i] + c[i] * ds[i];
-        c[i] = nc;
+    for (int j = j0; j < j0 + ONCE && j < STEPS; ++j) {
+      const int t = place(j);
+      if (t >= used && t < fill) {
+        if (F32 || un.turns) {
+          float x[8];
+          numbers_of_unit<F32>(raw[j - j0], x);
+          if (un.turns) turn_unit(x, turn.c, turn.s, r.interleaved);
+          pack_unit(x, w[j]);
+        } else {
+          w[j][0] = raw[j - j0].lo[0];
+          w[j][1] = raw[j - j0].lo[1];
+          w[j][2] = raw[j - j0].hi[0];
+          w[j][3] = raw[j - j0].hi[1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a = w[j][i] & 0x7fffu, d = (w[j][i] >> 16) & 0x7fffu;
+          top = a < 0x7f80u && a > top ? a : top;
+          top = d < 0x7f80u && d > top ? d : top;
+        }
       }
+      if (un.turns && j + 1 < STEPS) turn.advance(step);
     }
   }
   for (int off = 32; off > 0; off >>= 1) {
@@ -250,31 +273,55 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch
   // ---- the new codes
   const float rs = now > 0.f ? 1.f / now : 0.f;
   const bool through_lds = is_v && fill - used >= 16;
+  // a dim's row in LDS is turned by a multiple of eight dims' distance, so
+  // that the lanes of a wave, eight dims apart, meet different banks
+  constexpr int SKEW = 64 / U, WORDS = BLOCK / 4;
 #pragma unroll
-  for (int j = 0; j < STEPS; ++j) {
-    const int t = slot + j * SLOTS;
-    if (t < used || t >= fill) continue;
-    uint32_t out[2];
+  for (int j0 = 0; j0 < STEPS; j0 += G) {
+    uint32_t out[G][2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float y[4];
+    for (int j = j0; j < j0 + G; ++j) {
+      const int t = place(j);
+      out[j - j0][0] = out[j - j0][1] = 0;
+      if (t < used || t >= fill) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t pair = w[j][2 * half + (i >> 1)];
-        const uint32_t bits = (i & 1) ? pair >> 16 : pair & 0xffffu;
-        y[i] = now > 0.f ? code_quotient(bits, now, rs) : 0.f;
+      for (int half = 0; half < 2; ++half) {
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t pair = w[j][2 * half + (i >> 1)];
+          const uint32_t bits = (i & 1) ? pair >> 16 : pair & 0xffffu;
+          y[i] = now > 0.f ? code_quotient(bits, now, rs) : 0.f;
+        }
+        out[j - j0][half] = codes_of(y, e4m3);
       }
-      out[half] = codes_of(y, e4m3);
-    }
-    if (!is_v) {
-      *reinterpret_cast<uint32_t*>(codes + t * DIM + un.lo) = out[0];
-      *reinterpret_cast<uint32_t*>(codes + t * DIM + un.hi) = out[1];
-    } else {
-      uint8_t* to = through_lds ? reinterpret_cast<uint8_t*>(tile) : codes;
-      const int pitch = through_lds ? PITCH : BLOCK;
+      if (!is_v) {
+        *reinterpret_cast<uint32_t*>(codes + t * DIM + un.lo) = out[j - j0][0];
+        *reinterpret_cast<uint32_t*>(codes + t * DIM + un.hi) = out[j - j0][1];
+      } else if (!through_lds) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        to[(8 * u + i) * pitch + t] = (uint8_t)(out[i >> 2] >> (8 * (i & 3)));
+        for (int i = 0; i < 8; ++i)
+          codes[(8 * u + i) * BLOCK + t] = (uint8_t)(out[j - j0][i >> 2] >> (8 * (i & 3)));
+      }
+    }
+    if (through_lds) {
+      const int t = place(j0);
+      const int word = ((t >> 2) + SKEW * (u >> 3)) & (WORDS - 1);
+      uint8_t* to = reinterpret_cast<uint8_t*>(tile) + 8 * u * PITCH + 4 * word + (t & 3);
+      if (t < BLOCK) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t p = 0;
+#pragma unroll
+          for (int j = 0; j < G; ++j) p |= ((out[j][i >> 2] >> (8 * (i & 3))) & 0xffu) << (8 * j);
+          if (G == 4)
+            *reinterpret_cast<uint32_t*>(to + i * PITCH) = p;
+          else if (G == 2)
+            *reinterpret_cast<uint16_t*>(to + i * PITCH) = (uint16_t)p;
+          else
+            to[i * PITCH] = (uint8_t)p;
+        }
+      }
     }
   }
   if (!through_lds) return;
@@ -284,7 +331,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch
     if (t + 16 <= used || t >= fill) continue;
     uint32_t p[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = tile[(d * PITCH + t) / 4 + e];
+    for (int e = 0; e < 4; ++e)
+      p[e] = tile[d * (PITCH / 4) + (((t >> 2) + e + SKEW * (d >> 6)) & (WORDS - 1))];
     uint8_t* to = codes + d * BLOCK + t;
     if (t >= used && t + 16 <= fill) {
       *reinterpret_cast<u32x4*>(to) = u32x4{p[0], p[1], p[2], p[3]};
@@ -311,8 +359,12 @@ hipError_t append_dim(const KvCache& c, const KvBatch& b, const RopeSpec& r, con
                   (unsigned)b.seqs);
 #define MQ_APPEND(BLOCK)                                                                        \
   case BLOCK:                                                                                   \
-    hipLaunchKernelGGL((append_kernel<DIM, BLOCK>), grid, dim3(kThreads), 0, s, c, b, r, k, v,  \
-                       kv_stride, q, q_stride, q_heads, f32, q_out);                            \
+    if (f32)                                                                                    \
+      hipLaunchKernelGGL((append_kernel<DIM, BLOCK, true>), grid, dim3(kThreads), 0, s, c, b,   \
+                         r, k, v, kv_stride, q, q_stride, q_heads, q_out);                      \
+    else                                                                                        \
+      hipLaunchKernelGGL((append_kernel<DIM, BLOCK, false>), grid, dim3(kThreads), 0, s, c, b,  \
+                         r, k, v, kv_stride, q, q_stride, q_heads, q_out);                      \
     break
   switch (c.block) {
     MQ_APPEND(16);

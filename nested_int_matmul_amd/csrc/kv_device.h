@@ -173,28 +173,39 @@ __device__ __forceinline__ Unit unit_of(int u, int rot, bool interleaved) {
   return r;
 }
 
-// The unit's eight entries, from bf16 or fp32.
-__device__ __forceinline__ void load_unit(const void* x, bool f32, int64_t at, const Unit& u,
-                                          float* v) {
-  if (f32) {
+// The unit's eight entries as loaded (bf16: four dwords, fp32: eight), so that
+// several units can be in flight before the first is used, and as numbers.
+template <bool F32>
+struct RawUnit {
+  u32x4 lo, hi;  // bf16: the first two dwords of each
+};
+template <bool F32>
+__device__ __forceinline__ RawUnit<F32> load_unit(const void* x, int64_t at, const Unit& u) {
+  RawUnit<F32> r;
+  if (F32) {
     const float* p = static_cast<const float*>(x) + at;
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p + u.lo);
-    const f32x4 b = *reinterpret_cast<const f32x4*>(p + u.hi);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[4 + i] = b[i];
-    }
+    r.lo = *reinterpret_cast<const u32x4*>(p + u.lo);
+    r.hi = *reinterpret_cast<const u32x4*>(p + u.hi);
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(x) + at;
     const u32x2 a = *reinterpret_cast<const u32x2*>(p + u.lo);
     const u32x2 b = *reinterpret_cast<const u32x2*>(p + u.hi);
+    r.lo = u32x4{a[0], a[1], 0, 0};
+    r.hi = u32x4{b[0], b[1], 0, 0};
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void numbers_of_unit(const RawUnit<F32>& r, float* v) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      v[2 * i] = __uint_as_float(a[i] << 16);
-      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-      v[4 + 2 * i] = __uint_as_float(b[i] << 16);
-      v[4 + 2 * i + 1] = __uint_as_float(b[i] & 0xffff0000u);
+  for (int i = 0; i < 4; ++i) {
+    if (F32) {
+      v[i] = __uint_as_float(r.lo[i]);
+      v[4 + i] = __uint_as_float(r.hi[i]);
+    } else {
+      const uint32_t a = r.lo[i >> 1], b = r.hi[i >> 1];
+      v[i] = __uint_as_float((i & 1) ? a & 0xffff0000u : a << 16);
+      v[4 + i] = __uint_as_float((i & 1) ? b & 0xffff0000u : b << 16);
     }
   }
 }
@@ -211,6 +222,29 @@ __device__ __forceinline__ void turn_unit(float* v, const double* c, const doubl
     v[i2] = (float)(x2 * c[i] + x1 * s[i]);
   }
 }
+
+// Sines and cosines of a unit's four pairs at one position, times the factor;
+// and of a step of positions, by which advance() moves them on (one complex
+// product in float64, so a few of them in a row stay below 2^-48).
+struct Turn {
+  double c[4], s[4];
+  __device__ __forceinline__ void at(const RopeSpec& r, const Unit& u, double pos, double factor) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sincos64(pos * r.freq[u.pair0 + i], &s[i], &c[i]);
+      s[i] *= factor;
+      c[i] *= factor;
+    }
+  }
+  __device__ __forceinline__ void advance(const Turn& d) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double n = c[i] * d.c[i] - s[i] * d.s[i];
+      s[i] = s[i] * d.c[i] + c[i] * d.s[i];
+      c[i] = n;
+    }
+  }
+};
 
 // fp32 -> bf16 bits, nearest even; NaN stays a NaN.
 __device__ __forceinline__ uint32_t bf16_rne(float f) {
