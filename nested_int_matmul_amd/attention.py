@@ -22,7 +22,7 @@ from __future__ import annotations
 import ctypes
 import math
 
-from . import MQ_OK, MQError, _check, _need, _ptr, _same_device, _stream, lib
+from . import MQ_OK, MQError, _need, lib
 
 KV_FORMATS = {"int8": 0, "e4m3": 1}
 _BF16, _F32 = 0, 1
@@ -77,17 +77,38 @@ def declare(L):
 
 
 # ---------------------------------------------------------------- argument checks
+#
+# A decode step makes these calls at the rate of launches, so each tensor is
+# looked at once and addresses go to ctypes as plain integers.
 
-def _on_current(t, stream):
-    """Work is launched on the current device: the tensors have to be there,
-    and a stream given has to be one of it."""
+def _address(t, name, dtypes, device, shape=None):
+    """Address of a contiguous tensor on `device` of one of the types."""
+    _need(t, name, dtypes, shape=shape)
+    if t.device != device:
+        if not t.is_cuda:
+            raise ValueError("mq: tensors must be on the GPU")
+        raise ValueError(f"mq: {name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"mq: {name} must be contiguous (row-major)")
+    return t.data_ptr()
+
+
+def _launch_on(t, stream):
+    """Address of the stream to launch on.  Work is launched on the current
+    device: the tensors have to be there, and a stream given has to be its."""
     import torch
 
-    if t.device.index != torch.cuda.current_device():
+    if not t.is_cuda:
+        raise ValueError("mq: tensors must be on the GPU")
+    index = t.get_device()
+    if index != torch.cuda.current_device():
         raise ValueError(f"mq: tensors on {t.device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    if stream is not None and stream.device != t.device:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device != t.device:
         raise ValueError(f"mq: a stream of {stream.device} for tensors on {t.device}")
+    return stream.cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -101,30 +122,44 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows_view(x, name, heads=None, dim=None, rows=None):
-    """x [rows, heads, dim] whose rows are contiguous and evenly spaced (it may
-    be a part of wider rows): (type, row stride in entries)."""
+def _rows_view(x, name, device, heads=None, dim=None, rows=None):
+    """x bf16 or fp32 [rows, heads, dim] on `device` whose rows are contiguous
+    and evenly spaced (it may be a part of wider rows): (type, row stride in
+    entries, address)."""
     import torch
 
-    _need(x, name, (torch.bfloat16, torch.float32))
-    if x.dim() != 3:
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"mq: {name} must be a tensor")
+    kind = _F32 if x.dtype is torch.float32 else _BF16
+    if kind == _BF16 and x.dtype is not torch.bfloat16:
+        raise TypeError(f"mq: {name} has dtype {x.dtype}, expected bfloat16 or float32")
+    shape = x.shape
+    if len(shape) != 3:
         raise ValueError(f"mq: {name} must be [rows, heads, dim]")
-    if not x.is_cuda:
-        raise ValueError("mq: tensors must be on the GPU")
-    t, h, d = x.shape
-    for got, want, what in ((t, rows, "rows"), (h, heads, "heads"), (d, dim, "dim")):
-        if want is not None and got != want:
-            raise ValueError(f"mq: {name} has {got} {what}, expected {want}")
-    if (d > 1 and x.stride(2) != 1) or (h > 1 and x.stride(1) != d):
+    if x.device != device:
+        if not x.is_cuda:
+            raise ValueError("mq: tensors must be on the GPU")
+        raise ValueError(f"mq: {name} is on {x.device}, expected {device}")
+    t, h, d = shape
+    if (heads is not None and h != heads) or (dim is not None and d != dim) or \
+            (rows is not None and t != rows):
+        want = tuple("any" if v is None else v for v in (rows, heads, dim))
+        raise ValueError(f"mq: {name} has shape {tuple(shape)}, expected {want}")
+    s0, s1, s2 = x.stride()
+    if (d > 1 and s2 != 1) or (h > 1 and s1 != d):
         raise ValueError(f"mq: the rows of {name} must be contiguous")
-    stride = x.stride(0) if t > 1 else h * d
-    if stride < h * d:
+    if t <= 1:
+        s0 = h * d
+    elif s0 < h * d:
         raise ValueError(f"mq: the rows of {name} overlap")
-    return (_F32 if x.dtype == torch.float32 else _BF16), stride
+    return kind, s0, x.data_ptr()
 
 
-def _addr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _run(fn, name, args, rows):
+    if rows:  # (no rows: nothing to do, and empty tensors have no address)
+        st = fn(*args)
+        if st != MQ_OK:
+            raise MQError(st, name)
 
 
 # ---------------------------------------------------------------- what a user keeps
@@ -190,7 +225,11 @@ class Rope:
             raise ValueError("mq: freq must be [rot / 2]")
         self.freq, self.factor, self.interleaved = freq, float(factor), bool(interleaved)
         self.rot = 2 * freq.numel()
-        self.spec = _RopeSpec(_ptr(freq), self.factor, self.rot, int(self.interleaved))
+        if not freq.is_cuda:
+            raise ValueError("mq: tensors must be on the GPU")
+        self.spec = _RopeSpec(_address(freq, "freq", (torch.float64,), freq.device), self.factor,
+                              self.rot, int(self.interleaved))
+        self.device, self.ref = freq.device, ctypes.byref(self.spec)
 
 
 class KVCache:
@@ -201,20 +240,26 @@ class KVCache:
     def __init__(self, k, v, k_scale, v_scale, fmt: str):
         import torch
 
-        if fmt not in KV_FORMATS:
-            raise ValueError(f"mq: unknown cache format {fmt!r}")
         _need(k, "k", (torch.uint8,))
         if k.dim() != 4:
             raise ValueError("mq: k must be [pages, heads, block, dim]")
         p, h, b, d = k.shape
+        dev = k.device
+        if fmt not in KV_FORMATS:
+            raise ValueError(f"mq: unknown cache format {fmt!r}")
         _need(v, "v", (torch.uint8,), shape=(p, h, d, b))
         _need(k_scale, "k_scale", (torch.float32,), shape=(p, h))
         _need(v_scale, "v_scale", (torch.float32,), shape=(p, h))
-        _same_device(k, v, k_scale, v_scale)
+        if not k.is_cuda:
+            raise ValueError("mq: tensors must be on the GPU")
         self.k, self.v, self.k_scale, self.v_scale, self.fmt = k, v, k_scale, v_scale, fmt
-        self.pages, self.heads, self.block, self.dim = p, h, b, d
-        self.c = _Cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), p, h, b, d,
+        self.pages, self.heads, self.block, self.dim, self.device = p, h, b, d, dev
+        self.c = _Cache(_address(k, "k", (torch.uint8,), dev),
+                        _address(v, "v", (torch.uint8,), dev),
+                        _address(k_scale, "k_scale", (torch.float32,), dev),
+                        _address(v_scale, "v_scale", (torch.float32,), dev), p, h, b, d,
                         KV_FORMATS[fmt])
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def allocate(cls, pages: int, heads: int, block: int, dim: int, fmt: str = "int8",
@@ -244,89 +289,101 @@ class KVBatch:
         s, wide = page_table.shape
         _need(q_start, "q_start", i32, shape=(s + 1,))
         _need(kv_len, "kv_len", i32, shape=(s,))
-        _same_device(q_start, kv_len, page_table)
+        dev = q_start.device
         self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
         self.rows, self.max_new, self.seqs = int(rows), int(max_new), s
         if not (0 <= self.rows < 1 << 31 and 1 <= self.max_new < 1 << 31):
             raise ValueError("mq: rows or max_new out of range")
-        self.c = _Batch(_ptr(q_start), _ptr(kv_len), _ptr(page_table), self.rows, s, wide,
+        if not q_start.is_cuda:
+            raise ValueError("mq: tensors must be on the GPU")
+        self.device = dev
+        self.c = _Batch(_address(q_start, "q_start", i32, dev),
+                        _address(kv_len, "kv_len", i32, dev),
+                        _address(page_table, "page_table", i32, dev), self.rows, s, wide,
                         self.max_new)
+        self.ref = ctypes.byref(self.c)
 
 
 class _Plan:
-    """A checked and marshalled call: fn(*args), then `result`."""
+    """A checked and marshalled call: calling it makes the C call and returns
+    `result`.  `keep`: what the addresses belong to."""
 
-    def _set(self, fn, name, args, result, keep, rows):
-        self.fn, self.name, self.args, self.result = fn, name, args, result
-        self.keep, self.rows = keep, rows
+    def __init__(self, fn, name, args, rows, result, keep):
+        self.fn, self.name, self.args, self.rows = fn, name, args, rows
+        self.result, self.keep = result, keep
 
     def __call__(self):
-        if self.rows:
-            st = self.fn(*self.args)
-            if st != MQ_OK:
-                raise MQError(st, self.name)
+        _run(self.fn, self.name, self.args, self.rows)
         return self.result
+
+
+def _one_device(device, *others):
+    for o in others:
+        if o is not None and o.device != device:
+            raise ValueError(f"mq: tensors on different devices: {device} and {o.device}")
 
 
 # ---------------------------------------------------------------- the calls
 
-class RopePlan(_Plan):
-    """A prepared rope(): call it to rotate what x holds then; returns out."""
+def _rope_call(x, rope, positions, out, stream):
+    import torch
 
-    def __init__(self, x, rope: Rope, positions, out=None, stream=None):
-        import torch
-
-        kind, stride = _rows_view(x, "x")
-        t, h, d = x.shape
-        _need(positions, "positions", (torch.int32,), shape=(t,))
-        _on_current(x, stream)
-        if out is None:
-            out = _empty((t, h, d), torch.bfloat16, x.device, stream)
-        _need(out, "out", (torch.bfloat16,), shape=(t, h, d))
-        _, out_stride = _rows_view(out, "out")
-        _same_device(x, positions, out, rope.freq)
-        self._set(lib().mq_rope, "mq_rope",
-                  (ctypes.byref(rope.spec), _ptr(positions), _addr(x), kind, stride, t, h, d,
-                   _addr(out), out_stride, _stream(stream)), out, (x, rope, positions, out), t)
+    at = _launch_on(x, stream)
+    dev = x.device
+    kind, stride, px = _rows_view(x, "x", dev)
+    t, h, d = x.shape
+    pp = _address(positions, "positions", (torch.int32,), dev, (t,))
+    _one_device(dev, rope)
+    if out is None:
+        out = _empty((t, h, d), torch.bfloat16, dev, stream)
+    kind_out, out_stride, po = _rows_view(out, "out", dev, h, d, t)
+    if kind_out != _BF16:
+        raise TypeError("mq: out must be bf16")
+    return (rope.ref, pp, px, kind, stride, t, h, d, po, out_stride, at), t, out
 
 
 def rope(x, rope: Rope, positions, out=None, stream=None):
     """Rotary positions: x bf16 or fp32 [rows, heads, dim] (rows may be parts of
     wider ones), positions int32 [rows] -> bf16 [rows, heads, dim].  out may be
     x itself (bf16)."""
-    return RopePlan(x, rope, positions, out, stream)()
+    args, t, out = _rope_call(x, rope, positions, out, stream)
+    _run(lib().mq_rope, "mq_rope", args, t)
+    return out
 
 
-class CacheAppendPlan(_Plan):
-    """A prepared cache_append(); returns q_out (None without q)."""
+class RopePlan(_Plan):
+    """A prepared rope(): call it to rotate what x holds then; returns out."""
 
-    def __init__(self, cache: KVCache, batch: KVBatch, k, v, q=None, rope: Rope = None, q_out=None,
-                 stream=None):
-        import torch
+    def __init__(self, x, rope: Rope, positions, out=None, stream=None):
+        args, t, out = _rope_call(x, rope, positions, out, stream)
+        super().__init__(lib().mq_rope, "mq_rope", args, t, out, (x, rope, positions))
 
-        kind, stride = _rows_view(k, "k", cache.heads, cache.dim, batch.rows)
-        kind_v, stride_v = _rows_view(v, "v", cache.heads, cache.dim, batch.rows)
-        if (kind, stride) != (kind_v, stride_v):
-            raise ValueError("mq: k and v need one type and one row stride")
-        _on_current(k, stream)
-        q_stride = q_heads = 0
-        if q is not None:
-            kind_q, q_stride = _rows_view(q, "q", None, cache.dim, batch.rows)
-            if kind_q != kind:
-                raise TypeError("mq: q has another type than k and v")
-            q_heads = q.shape[1]
-            if q_out is None:
-                q_out = _empty(tuple(q.shape), torch.bfloat16, q.device, stream)
-            _need(q_out, "q_out", (torch.bfloat16,), shape=tuple(q.shape))
-            _ptr(q_out)
-        elif q_out is not None:
-            raise ValueError("mq: q_out without q")
-        _same_device(k, v, q, q_out, cache.k, batch.q_start, rope.freq if rope else None)
-        self._set(lib().mq_cache_append, "mq_cache_append",
-                  (ctypes.byref(cache.c), ctypes.byref(batch.c),
-                   ctypes.byref(rope.spec) if rope else None, _addr(k), _addr(v), stride, _addr(q),
-                   q_stride, q_heads, kind, _addr(q_out), _stream(stream)), q_out,
-                  (cache, batch, k, v, q, rope, q_out), batch.rows)
+
+def _append_call(cache, batch, k, v, q, rope, q_out, stream):
+    import torch
+
+    at = _launch_on(k, stream)
+    dev = k.device
+    rows, dim = batch.rows, cache.dim
+    kind, stride, pk = _rows_view(k, "k", dev, cache.heads, dim, rows)
+    kind_v, stride_v, pv = _rows_view(v, "v", dev, cache.heads, dim, rows)
+    if (kind, stride) != (kind_v, stride_v):
+        raise ValueError("mq: k and v need one type and one row stride")
+    _one_device(dev, cache, batch, rope)
+    q_stride, q_heads, pq, po = 0, 0, None, None
+    if q is not None:
+        kind_q, q_stride, pq = _rows_view(q, "q", dev, None, dim, rows)
+        if kind_q != kind:
+            raise TypeError("mq: q has another type than k and v")
+        shape = tuple(q.shape)
+        q_heads = shape[1]
+        if q_out is None:
+            q_out = _empty(shape, torch.bfloat16, dev, stream)
+        po = _address(q_out, "q_out", (torch.bfloat16,), dev, shape)
+    elif q_out is not None:
+        raise ValueError("mq: q_out without q")
+    return (cache.ref, batch.ref, rope.ref if rope is not None else None, pk, pv, stride, pq,
+            q_stride, q_heads, kind, po, at), rows, q_out
 
 
 def cache_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope: Rope = None, q_out=None,
@@ -334,8 +391,20 @@ def cache_append(cache: KVCache, batch: KVBatch, k, v, q=None, rope: Rope = None
     """Quantize the batch's rows of k and v (bf16 or fp32 [rows, heads, dim])
     into the cache; with `rope` k is rotated by its position first.  With q
     [rows, q_heads, dim] the queries are rotated in the same launch and
-    returned as bf16."""
-    return CacheAppendPlan(cache, batch, k, v, q, rope, q_out, stream)()
+    returned as bf16 (in q_out)."""
+    args, rows, q_out = _append_call(cache, batch, k, v, q, rope, q_out, stream)
+    _run(lib().mq_cache_append, "mq_cache_append", args, rows)
+    return q_out
+
+
+class CacheAppendPlan(_Plan):
+    """A prepared cache_append(); returns q_out (None without q)."""
+
+    def __init__(self, cache: KVCache, batch: KVBatch, k, v, q=None, rope: Rope = None, q_out=None,
+                 stream=None):
+        args, rows, q_out = _append_call(cache, batch, k, v, q, rope, q_out, stream)
+        super().__init__(lib().mq_cache_append, "mq_cache_append", args, rows, q_out,
+                         (cache, batch, k, v, q, rope))
 
 
 def cache_read(cache: KVCache, batch: KVBatch, dtype=None, k_out=None, v_out=None, stream=None):
@@ -345,62 +414,51 @@ def cache_read(cache: KVCache, batch: KVBatch, dtype=None, k_out=None, v_out=Non
 
     if dtype is None:
         dtype = torch.bfloat16 if k_out is None else k_out.dtype
-    if dtype not in (torch.bfloat16, torch.float32):
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError("mq: the cache is read as bf16 or fp32")
+    at = _launch_on(cache.k, stream)
+    dev = cache.device
+    _one_device(dev, batch)
     shape = (batch.rows, cache.heads, cache.dim)
-    _on_current(cache.k, stream)
     if k_out is None:
-        k_out = _empty(shape, dtype, cache.k.device, stream)
+        k_out = _empty(shape, dtype, dev, stream)
     if v_out is None:
-        v_out = _empty(shape, dtype, cache.k.device, stream)
-    _need(k_out, "k_out", (dtype,), shape=shape)
-    _need(v_out, "v_out", (dtype,), shape=shape)
-    _same_device(cache.k, batch.q_start, k_out, v_out)
-    if batch.rows:
-        _check(lib().mq_cache_read(ctypes.byref(cache.c), ctypes.byref(batch.c), _ptr(k_out),
-                                   _ptr(v_out), _F32 if dtype == torch.float32 else _BF16,
-                                   _stream(stream)), "mq_cache_read")
+        v_out = _empty(shape, dtype, dev, stream)
+    args = (cache.ref, batch.ref, _address(k_out, "k_out", (dtype,), dev, shape),
+            _address(v_out, "v_out", (dtype,), dev, shape),
+            _F32 if dtype is torch.float32 else _BF16, at)
+    _run(lib().mq_cache_read, "mq_cache_read", args, batch.rows)
     return k_out, v_out
 
 
 def cache_attend_workspace_bytes(cache: KVCache, batch: KVBatch, q_heads: int,
                                  window: int = 0) -> int:
-    return int(lib().mq_cache_attend_workspace_bytes(ctypes.byref(cache.c), ctypes.byref(batch.c),
-                                                     q_heads, window))
+    return int(lib().mq_cache_attend_workspace_bytes(cache.ref, batch.ref, q_heads, window))
 
 
-class CacheAttendPlan(_Plan):
-    """A prepared cache_attend(); returns out, or (out, lse) if lse was given.
-    Its workspace is its own unless one is given."""
+def _attend_call(cache, batch, q, scale, softcap, window, causal, out, lse, workspace, stream):
+    import torch
 
-    def __init__(self, cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0,
-                 window: int = 0, causal: bool = True, out=None, lse=None, workspace=None,
-                 stream=None):
-        import torch
-
-        _need(q, "q", (torch.bfloat16,))
-        _, stride = _rows_view(q, "q", None, cache.dim, batch.rows)
-        t, h, d = q.shape
-        _on_current(q, stream)
-        if out is None:
-            out = _empty((t, h, d), torch.bfloat16, q.device, stream)
-        _need(out, "out", (torch.bfloat16,), shape=(t, h, d))
-        if lse is not None:
-            _need(lse, "lse", (torch.float32,), shape=(t, h))
+    at = _launch_on(q, stream)
+    dev = q.device
+    kind, stride, pq = _rows_view(q, "q", dev, None, cache.dim, batch.rows)
+    if kind != _BF16:
+        raise TypeError("mq: q must be bf16")
+    _one_device(dev, cache, batch)
+    t, h, d = q.shape
+    if out is None:
+        out = _empty((t, h, d), torch.bfloat16, dev, stream)
+    po = _address(out, "out", (torch.bfloat16,), dev, (t, h, d))
+    pl = None if lse is None else _address(lse, "lse", (torch.float32,), dev, (t, h))
+    if workspace is None:
         need = cache_attend_workspace_bytes(cache, batch, h, window)
-        if need and workspace is None:
-            workspace = _empty((need,), torch.uint8, q.device, stream)
-        if workspace is not None:
-            _need(workspace, "workspace", (torch.uint8,))
-        _same_device(q, out, lse, workspace, cache.k, batch.q_start)
-        ws_bytes = 0 if workspace is None else workspace.numel()
-        _ptr(out), _ptr(lse)
-        self._set(lib().mq_cache_attend, "mq_cache_attend",
-                  (ctypes.byref(cache.c), ctypes.byref(batch.c), _addr(q), stride, h,
-                   float(d ** -0.5 if scale is None else scale), float(softcap), int(window),
-                   int(bool(causal)), _addr(out), _addr(lse), _ptr(workspace), ws_bytes,
-                   _stream(stream)),
-                  out if lse is None else (out, lse), (cache, batch, q, out, lse, workspace), t)
+        if need:
+            workspace = _empty((need,), torch.uint8, dev, stream)
+    pw, nw = None, 0
+    if workspace is not None:
+        pw, nw = _address(workspace, "workspace", (torch.uint8,), dev), workspace.numel()
+    return (cache.ref, batch.ref, pq, stride, h, d ** -0.5 if scale is None else scale, softcap,
+            window, 1 if causal else 0, po, pl, pw, nw, at), t, out, workspace
 
 
 def cache_attend(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0,
@@ -410,10 +468,23 @@ def cache_attend(cache: KVCache, batch: KVBatch, q, scale=None, softcap: float =
     sequences' cached tokens -> bf16 [rows, q_heads, dim].  scale: dim^-0.5 by
     default; softcap > 0 caps the scores; window > 0: only the last `window`
     tokens up to the query; lse: fp32 [rows, q_heads], filled if given."""
-    plan = CacheAttendPlan(cache, batch, q, scale, softcap, window, causal, out, lse, workspace,
-                           stream)
-    plan()
-    return plan.result if lse is None else plan.result[0]
+    args, t, out, _ = _attend_call(cache, batch, q, scale, softcap, window, causal, out, lse,
+                                   workspace, stream)
+    _run(lib().mq_cache_attend, "mq_cache_attend", args, t)
+    return out
+
+
+class CacheAttendPlan(_Plan):
+    """A prepared cache_attend(); returns out, or (out, lse) if lse was given.
+    Its workspace is its own unless one is given."""
+
+    def __init__(self, cache: KVCache, batch: KVBatch, q, scale=None, softcap: float = 0.0,
+                 window: int = 0, causal: bool = True, out=None, lse=None, workspace=None,
+                 stream=None):
+        args, t, out, workspace = _attend_call(cache, batch, q, scale, softcap, window, causal, out,
+                                               lse, workspace, stream)
+        super().__init__(lib().mq_cache_attend, "mq_cache_attend", args, t,
+                         out if lse is None else (out, lse), (cache, batch, q, workspace))
 
 
 class StackAttention:
@@ -429,7 +500,7 @@ class StackAttention:
         if windows is not None and len(windows) != len(self.caches):
             raise ValueError("mq: one window a layer")
         self.q_heads = int(q_heads)
-        _same_device(batch.q_start, rope.freq if rope else None, *(c.k for c in self.caches))
+        _one_device(batch.device, rope, *self.caches)
         self._arr = (_Cache * len(self.caches))(*(c.c for c in self.caches))
         self._win = None if windows is None else (ctypes.c_int64 * len(windows))(*windows)
         self.c = _StackAttention(
@@ -457,19 +528,21 @@ def mixnmatch_attend(layer_arr, attn: StackAttention, x=None, h=None, workspace=
     width = int(layer_arr[0].q.N) if len(layer_arr) else 0
     if H != width or m != attn.batch.rows:
         raise ValueError(f"mq: the input is [{m}, {H}], expected [{attn.batch.rows}, {width}]")
-    dev = (x if x is not None else h).device
+    first = x if x is not None else h
+    at, dev = _launch_on(first, stream), first.device
+    _one_device(dev, attn.batch)
+    px = None
     if x is not None:
-        _need(x, "x", (torch.bfloat16, torch.int16, torch.uint16), shape=(m, H))
+        px = _address(x, "x", (torch.bfloat16, torch.int16, torch.uint16), dev, (m, H))
     if h is None:
         h = _empty((m, H), torch.float32, dev, stream)
-    _need(h, "h", (torch.float32,), shape=(m, H))
-    need = mixnmatch_attend_workspace_bytes(layer_arr, attn, m)
+    ph = _address(h, "h", (torch.float32,), dev, (m, H))
     if workspace is None:
+        need = mixnmatch_attend_workspace_bytes(layer_arr, attn, m)
         workspace = _empty((max(need, 1),), torch.uint8, dev, stream)
-    _need(workspace, "workspace", (torch.uint8,))
-    _same_device(x, h, workspace, attn.batch.q_start)
-    _on_current(h, stream)
-    _check(lib().mq_mixnmatch_attend(layer_arr, len(layer_arr), ctypes.byref(attn.c), _ptr(x), m,
-                                     _ptr(h), _ptr(workspace), workspace.numel(),
-                                     _stream(stream)), "mq_mixnmatch_attend")
+    pw = _address(workspace, "workspace", (torch.uint8,), dev)
+    if len(layer_arr) != len(attn.caches):
+        raise ValueError("mq: one cache a layer")
+    _run(lib().mq_mixnmatch_attend, "mq_mixnmatch_attend",
+         (layer_arr, len(layer_arr), ctypes.byref(attn.c), px, m, ph, pw, workspace.numel(), at), 1)
     return h
