@@ -29,11 +29,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeSpec r, const int* p
   const int h0 = blockIdx.y * per, h1 = h0 + per < heads ? h0 + per : heads;
   Turn turn;
   RawUnit<F32> raw[4];
+  const int pos = positions[row];
   for (int h = h0; h < h1; h += 4) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (h + j < h1) raw[j] = load_unit<F32>(x, row * x_stride + (int64_t)(h + j) * dim, un);
-    if (h == h0 && un.turns) turn.at(r, un, (double)positions[row], r.factor);
+    if (h == h0 && un.turns) turn.at(r, un, (double)pos, r.factor);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (h + j >= h1) continue;
@@ -72,12 +73,16 @@ hipError_t launch_rope(const RopeSpec& r, const int* positions, const void* x, b
 // --------------------------------------------------------- mq_cache_append
 //
 // One workgroup per (sequence, page that gets tokens, head, k or v): the
-// page's new values stay in registers as bf16 (at most 64 dwords a thread)
+// page's new values stay in registers as bf16 (at most 32 dwords a thread)
 // between finding the scale and rounding to codes, so they are read once, and
 // no other workgroup touches the page's scale or codes.  Eight tokens' loads
-// (four of fp32) are in flight before the first is used.  k's angles of a
-// thread advance by a constant step, so its sines and cosines follow by one
-// complex product a token in place of an evaluation.
+// (four of fp32) are in flight before the first is used, the first of them
+// before the page is known.  k's angles of a thread advance by a constant
+// step, so its sines and cosines follow by one complex product a token in
+// place of an evaluation.
+// Rounding: a product with 1 / scale decides unless the quotient is within its
+// error of a border between codes; only then is the exact quotient's side
+// found (exact_quotient).
 // v is held dim-major: pages that get 16 tokens or more go through LDS, four
 // tokens of a dim to a dword, and leave in 16-byte pieces; fewer tokens go out
 // as single bytes.
@@ -88,11 +93,11 @@ hipError_t launch_rope(const RopeSpec& r, const int* positions, const void* x, b
 constexpr int kQueryTokens = 8;
 
 // at most eight tokens of one page, all query heads
-template <int DIM, bool F32>
+template <int DIM, int T, bool F32>
 __device__ __forceinline__ void append_queries(const RopeSpec& r, const SeqSpan& sp, int64_t lo,
                                                int64_t hi, const void* q, int64_t q_stride,
                                                int q_heads, uint16_t* q_out) {
-  constexpr int U = DIM / 8, SLOTS = kThreads / U;
+  constexpr int U = DIM / 8, SLOTS = T / U;
   const int u = threadIdx.x % U, slot = threadIdx.x / U;
   const int hs = q_heads < SLOTS ? q_heads : SLOTS;  // heads side by side
   const int toks = SLOTS / hs;                       // tokens side by side
@@ -132,27 +137,40 @@ __device__ __forceinline__ void append_queries(const RopeSpec& r, const SeqSpan&
   }
 }
 
-// a bf16 pattern's value as a quotient's dividend, and whether it is a number
-__device__ __forceinline__ float code_quotient(uint32_t bits, float s, float rs) {
-  const uint32_t mag = bits & 0x7fffu;
-  if (mag >= 0x7f80u)  // infinity: beyond every code, NaN: 0
-    return mag > 0x7f80u ? 0.f : ((bits & 0x8000u) ? -1e9f : 1e9f);
-  return exact_quotient(__uint_as_float(bits << 16), s, rs);
+// Codes of a unit (four dwords of bf16 pairs) from exact quotients.
+__device__ __forceinline__ void exact_codes(const uint32_t* w, float s, float rs, bool e4m3,
+                                            uint32_t* out) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t pair = w[2 * h + (i >> 1)];
+      const uint32_t bits = (i & 1) ? pair >> 16 : pair & 0xffffu;
+      const uint32_t mag = bits & 0x7fffu;
+      y[i] = exact_quotient(__uint_as_float(bits << 16), s, rs);
+      if (mag >= 0x7f80u)  // infinity: beyond every code, NaN: 0
+        y[i] = mag > 0x7f80u ? 0.f : ((bits & 0x8000u) ? -1e9f : 1e9f);
+    }
+    out[h] = codes_of(y, e4m3);
+  }
 }
 
+// Threads of a page's workgroup: at most 64 values each.
+constexpr int append_threads(int dim, int block) { return dim * block > 16384 ? 512 : 256; }
+
 template <int DIM, int BLOCK, bool F32>
-__global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch b, RopeSpec r,
-                                                          const void* k, const void* v,
-                                                          int64_t kv_stride, const void* q,
-                                                          int64_t q_stride, int q_heads,
-                                                          uint16_t* q_out) {
-  constexpr int U = DIM / 8, SLOTS = kThreads / U;
+__global__ void __launch_bounds__(append_threads(DIM, BLOCK))
+append_kernel(KvCache cache, KvBatch b, RopeSpec r, const void* k, const void* v,
+              int64_t kv_stride, const void* q, int64_t q_stride, int q_heads, uint16_t* q_out) {
+  constexpr int T = append_threads(DIM, BLOCK);
+  constexpr int U = DIM / 8, SLOTS = T / U;
   constexpr int STEPS = BLOCK / SLOTS > 0 ? BLOCK / SLOTS : 1;
   constexpr int ONCE = F32 ? 4 : 8;            // steps loaded before the first is used
   constexpr int G = STEPS < 4 ? STEPS : 4;     // consecutive tokens a thread has of v
   constexpr int PITCH = BLOCK + 4;             // bytes of a dim's row in LDS
   __shared__ uint32_t tile[DIM * PITCH / 4];
-  __shared__ uint32_t wave_max[kThreads / 64];
+  __shared__ uint32_t wave_max[T / 64];
 
   const int seq = blockIdx.z;
   const SeqSpan sp = seq_span(b, seq);
@@ -169,21 +187,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch
     lo = lo > base + part * kQueryTokens ? lo : base + part * kQueryTokens;
     const int64_t last = base + (part + 1) * kQueryTokens;
     hi = hi < last ? hi : last;
-    if (lo < hi) append_queries<DIM, F32>(r, sp, lo, hi, q, q_stride, q_heads, q_out);
+    if (lo < hi) append_queries<DIM, T, F32>(r, sp, lo, hi, q, q_stride, q_heads, q_out);
     return;
   }
   const int page = page_of(b, seq, pi, cache.pages);
-  if (page < 0) return;
   const int head = blockIdx.y >> 1;
   const bool is_v = blockIdx.y & 1;
   const bool e4m3 = cache.e4m3;
   const int tid = threadIdx.x, u = tid % U, slot = tid / U;
-  const int64_t ph = (int64_t)page * cache.heads + head;
-  float* scale_at = (is_v ? cache.v_scale : cache.k_scale) + ph;
-  uint8_t* codes = (is_v ? cache.v : cache.k) + ph * (DIM * BLOCK);
   const int used = (int)(lo - base);  // earlier tokens of the page
   const int fill = (int)(hi - base);
-  const float was = used > 0 ? *scale_at : 0.f;
 
   // ---- the page's new values as bf16, and their largest magnitude
   const Unit un = is_v ? unit_of(u, 0, false) : unit_of(u, r.freq ? r.rot : 0, r.interleaved);
@@ -194,7 +207,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch
   const void* src = is_v ? v : k;
   const int64_t at0 = (sp.row0 + (base - sp.start)) * kv_stride + (int64_t)head * DIM;
   uint32_t w[STEPS][4];
-  uint32_t top = 0;
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 pair_top = {0, 0};
   Turn turn, step;
 #pragma unroll
   for (int j0 = 0; j0 < STEPS; j0 += ONCE) {
@@ -224,23 +238,45 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch
           w[j][3] = raw[j - j0].hi[1];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a = w[j][i] & 0x7fffu, d = (w[j][i] >> 16) & 0x7fffu;
-          top = a < 0x7f80u && a > top ? a : top;
-          top = d < 0x7f80u && d > top ? d : top;
-        }
+        for (int i = 0; i < 4; ++i)
+          pair_top = __builtin_elementwise_max(
+              pair_top, __builtin_bit_cast(u16x2, w[j][i] & 0x7fff7fffu));
       }
       if (un.turns && j + 1 < STEPS) turn.advance(step);
     }
   }
-  for (int off = 32; off > 0; off >>= 1) {
-    const uint32_t o = __shfl_xor(top, off);
-    top = o > top ? o : top;
-  }
-  if ((tid & 63) == 0) wave_max[tid >> 6] = top;
-  __syncthreads();
+  if (page < 0) return;  // (uniform: the page is the workgroup's)
+  const int64_t ph = (int64_t)page * cache.heads + head;
+  float* scale_at = (is_v ? cache.v_scale : cache.k_scale) + ph;
+  uint8_t* codes = (is_v ? cache.v : cache.k) + ph * (DIM * BLOCK);
+  const float was = used > 0 ? *scale_at : 0.f;
+  uint32_t top = pair_top[0] > pair_top[1] ? pair_top[0] : pair_top[1];
+  // the largest of the workgroup; if some value is no number, of the numbers
+  bool odd = false;
+  for (int round = 0; round < 2; ++round) {
+    for (int off = 32; off > 0; off >>= 1) {
+      const uint32_t o = __shfl_xor(top, off);
+      top = o > top ? o : top;
+    }
+    if (round > 0) __syncthreads();
+    if ((tid & 63) == 0) wave_max[tid >> 6] = top;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) top = wave_max[i] > top ? wave_max[i] : top;
+    for (int i = 0; i < T / 64; ++i) top = wave_max[i] > top ? wave_max[i] : top;
+    if (top < 0x7f80u) break;
+    odd = true;
+    top = 0;
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      const int t = place(j);
+      if (t < used || t >= fill) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t m = (w[j][i >> 1] >> (16 * (i & 1))) & 0x7fffu;
+        top = m < 0x7f80u && m > top ? m : top;
+      }
+    }
+  }
   float now = __uint_as_float(top << 16) * kv_inv_qmax(e4m3);
   if (now < kMinScale) now = 0.f;
   const bool grows = used > 0 && now > was;
@@ -250,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch
   // ---- earlier codes, where the scale grows
   if (grows) {
     if (!is_v) {
-      for (int i = tid; i < used * (DIM / 4); i += kThreads) {
+      for (int i = tid; i < used * (DIM / 4); i += T) {
         uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
         *p = recode(*p, e4m3, was, now);
       }
@@ -258,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch
       // four tokens of a dim at a time; those at or beyond `used` keep their
       // bytes here (this workgroup writes them below)
       const int per = (used + 3) / 4;
-      for (int i = tid; i < per * DIM; i += kThreads) {
+      for (int i = tid; i < per * DIM; i += T) {
         const int d = i / per, t = (i % per) * 4;
         uint32_t* p = reinterpret_cast<uint32_t*>(codes + d * BLOCK + t);
         const uint32_t before = *p, after = recode(before, e4m3, was, now);
@@ -284,16 +320,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch
       const int t = place(j);
       out[j - j0][0] = out[j - j0][1] = 0;
       if (t < used || t >= fill) continue;
+      if (now > 0.f) {
+        float x[8];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t pair = w[j][2 * half + (i >> 1)];
-          const uint32_t bits = (i & 1) ? pair >> 16 : pair & 0xffffu;
-          y[i] = now > 0.f ? code_quotient(bits, now, rs) : 0.f;
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t pair = w[j][i >> 1];
+          x[i] = __uint_as_float((i & 1) ? pair & 0xffff0000u : pair << 16);
         }
-        out[j - j0][half] = codes_of(y, e4m3);
+        const bool near = quick_codes(x, rs, e4m3, out[j - j0]);
+        if (near || odd) exact_codes(w[j], now, rs, e4m3, out[j - j0]);
       }
       if (!is_v) {
         *reinterpret_cast<uint32_t*>(codes + t * DIM + un.lo) = out[j - j0][0];
@@ -326,7 +361,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvCache cache, KvBatch
   }
   if (!through_lds) return;
   __syncthreads();
-  for (int i = tid; i < DIM * (BLOCK / 16); i += kThreads) {
+  for (int i = tid; i < DIM * (BLOCK / 16); i += T) {
     const int d = i / (BLOCK / 16), t = (i % (BLOCK / 16)) * 16;
     if (t + 16 <= used || t >= fill) continue;
     uint32_t p[4];
@@ -360,10 +395,12 @@ hipError_t append_dim(const KvCache& c, const KvBatch& b, const RopeSpec& r, con
 #define MQ_APPEND(BLOCK)                                                                        \
   case BLOCK:                                                                                   \
     if (f32)                                                                                    \
-      hipLaunchKernelGGL((append_kernel<DIM, BLOCK, true>), grid, dim3(kThreads), 0, s, c, b,   \
+      hipLaunchKernelGGL((append_kernel<DIM, BLOCK, true>), grid,                               \
+                         dim3(append_threads(DIM, BLOCK)), 0, s, c, b,                          \
                          r, k, v, kv_stride, q, q_stride, q_heads, q_out);                      \
     else                                                                                        \
-      hipLaunchKernelGGL((append_kernel<DIM, BLOCK, false>), grid, dim3(kThreads), 0, s, c, b,  \
+      hipLaunchKernelGGL((append_kernel<DIM, BLOCK, false>), grid,                              \
+                         dim3(append_threads(DIM, BLOCK)), 0, s, c, b,                          \
                          r, k, v, kv_stride, q, q_stride, q_heads, q_out);                      \
     break
   switch (c.block) {

@@ -72,6 +72,52 @@ __device__ __forceinline__ float f64_to_f32_odd(double q) {
   return __int_as_float(bits);
 }
 
+// Quotients x * rs of eight values, good to 2^-23 of themselves, to code bytes,
+// and whether one of them is so near a border between two codes (or on it) that
+// only the exact quotient can tell.  For finite values up to the scale's range.
+__device__ __forceinline__ bool quick_codes(const float* x, float rs, bool e4m3, uint32_t* out) {
+  if (e4m3) {
+    // A border has one bit set below the three of a code's mantissa: in the
+    // low 20 bits of the quotient, or of 2^-6 plus it where codes are
+    // subnormal (their spacing is that of [2^-6, 2^-5)).  Four units in the
+    // last place on each side cover the error (two) and that sum's (one).
+    uint32_t near = 0xffffffffu;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] = x[4 * h + i] * rs;
+        const float m = fabsf(y[i]);
+        const float z = m < 0x1p-6f ? m + 0x1p-6f : m;
+        const uint32_t t = (__float_as_uint(z) + (4u - 0x80000u)) & 0xfffffu;
+        near = t < near ? t : near;
+      }
+      int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+      out[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+    }
+    return near <= 8u;
+  }
+  // 1.5 * 2^23 added rounds to the nearest integer, ties to even, and leaves
+  // it in the low byte; |y| <= 127 is off by less than 2^-16.
+  float worst = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float y = x[4 * h + i] * rs;
+      const float r = y + 12582912.f;
+      z[i] = __float_as_uint(r);
+      worst = fmaxf(worst, fabsf(y - (r - 12582912.f)));
+    }
+    const uint32_t a = __builtin_amdgcn_perm(z[1], z[0], 0x0c0c0400u);
+    const uint32_t b = __builtin_amdgcn_perm(z[3], z[2], 0x04000c0cu);
+    out[h] = a | b;
+  }
+  return worst >= 0.5f - 0x1p-15f;
+}
+
 // Four quotients (rounded to odd) to four code bytes.
 __device__ __forceinline__ uint32_t codes_of(const float* y, bool e4m3) {
   if (e4m3) {
