@@ -435,7 +435,7 @@ typedef struct mq_kv_cache {
  * block hold no token (nothing is written there, and attention sees no key),
  * rows beyond `rows` and tokens beyond max_new are not touched.
  * Sizes: 0 <= rows < 2^31, 1 <= seqs <= 65535, 1 <= table_pages,
- * table_pages * block < 2^31, 1 <= max_new <= 2^24; pointers 4-byte aligned.
+ * table_pages * block <= 2^30, 1 <= max_new <= 2^24; pointers 4-byte aligned.
  */
 typedef struct mq_kv_batch {
   const int32_t* q_start;
@@ -541,8 +541,8 @@ MQ_API mq_status mq_cache_read(const mq_kv_cache* cache, const mq_kv_batch* batc
  *              aligned (may be NULL when that is 0): partial results of long
  *              sequences cut into pieces.  Calls that may overlap in time
  *              need workspaces of their own.
- * Sizes: q_heads a multiple of heads, q_heads * dim <= 2^20;
- * max_new * q_heads <= 2^26; rows * q_heads < 2^31; q, out 16-byte aligned,
+ * Sizes: q_heads a multiple of heads, at most 1024 times it; q_heads * dim <=
+ * 2^20; max_new * q_heads <= 2^24; rows * q_heads < 2^31; q, out 16-byte aligned,
  * q_stride a multiple of 8 and >= q_heads * dim.
  */
 MQ_API size_t mq_cache_attend_workspace_bytes(const mq_kv_cache* cache, const mq_kv_batch* batch,

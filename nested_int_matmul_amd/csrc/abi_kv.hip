@@ -29,7 +29,7 @@ mq_status check_cache(const mq_kv_cache* c) {
 mq_status check_batch(const mq_kv_batch* b, const mq_kv_cache* c) {
   if (!b || !b->q_start || !b->kv_len || !b->page_table) return MQ_ERR_NULL;
   if (b->rows < 0 || b->rows > 0x7fffffff || b->seqs < 1 || b->seqs > 65535) return MQ_ERR_SHAPE;
-  if (b->table_pages < 1 || (int64_t)b->table_pages * c->block > 0x7fffffff) return MQ_ERR_SHAPE;
+  if (b->table_pages < 1 || (int64_t)b->table_pages * c->block > (int64_t)1 << 30) return MQ_ERR_SHAPE;
   if (b->max_new < 1 || b->max_new > kMaxNew) return MQ_ERR_SHAPE;
   if (misaligned(b->q_start, 4) || misaligned(b->kv_len, 4) || misaligned(b->page_table, 4))
     return MQ_ERR_ALIGN;
@@ -73,9 +73,10 @@ mq_status check_attend(const mq_kv_cache* c, const mq_kv_batch* b, int64_t q_hea
   if (s != MQ_OK) return s;
   s = check_batch(b, c);
   if (s != MQ_OK) return s;
-  if (q_heads < 1 || q_heads > kMaxRowEntries / c->dim || q_heads % c->heads != 0)
+  if (q_heads < 1 || q_heads > kMaxRowEntries / c->dim || q_heads % c->heads != 0 ||
+      q_heads / c->heads > 1024)
     return MQ_ERR_SHAPE;
-  if ((int64_t)b->max_new * q_heads > ((int64_t)1 << 26)) return MQ_ERR_SHAPE;
+  if ((int64_t)b->max_new * q_heads > (int64_t)1 << 24) return MQ_ERR_SHAPE;
   if (b->rows * q_heads > 0x7fffffff) return MQ_ERR_SHAPE;
   if (window < 0) return MQ_ERR_SHAPE;
   return MQ_OK;
@@ -88,6 +89,7 @@ mq::AttendArgs attend_args(const mq_kv_cache* c, const mq_kv_batch* b, int64_t q
   a.batch = batch_of(b);
   a.q_heads = (int)q_heads;
   a.group = (int)(q_heads / c->heads);
+  a.group_mul = (((uint64_t)1 << 36) + a.group - 1) / a.group;
   a.window = window < (int64_t)1 << 31 ? window : (int64_t)1 << 31;  // no position is beyond
   return a;
 }

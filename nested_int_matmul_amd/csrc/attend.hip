@@ -72,20 +72,22 @@ __device__ __forceinline__ void codes_to_f16(u32x4 w, f16x8* a, f16x8* b) {
 // 2^-29 of it).
 __device__ __forceinline__ float capped(float z) {
   const float e2 = __builtin_amdgcn_exp2f(2.f * kLog2e * fabsf(z));
-  const float big = copysignf(1.f - 2.f / (e2 + 1.f), z);
+  const float big = copysignf(fmaf(-2.f, __builtin_amdgcn_rcpf(e2 + 1.f), 1.f), z);
   const float zz = z * z;
   const float small = z * (1.f + zz * (-1.f / 3.f + zz * (2.f / 15.f + zz * (-17.f / 315.f))));
   return fabsf(z) < 0.125f ? small : big;
 }
 
-// Keys [lo, hi) of the token at position pos.
+// Keys [lo, hi) of the token at position pos (positions are below 2^30).
 struct Keys {
-  int64_t lo, hi;
+  int lo, hi;
 };
-__device__ __forceinline__ Keys keys_of(const AttendArgs& a, int64_t pos, int64_t held) {
+__device__ __forceinline__ Keys keys_of(const AttendArgs& a, int64_t pos, int held) {
   Keys k;
-  k.hi = a.causal && pos + 1 < held ? pos + 1 : held;
-  k.lo = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
+  k.hi = a.causal && pos + 1 < held ? (int)(pos + 1) : held;
+  k.lo = 0;
+  if (a.window > 0 && pos - a.window + 1 > 0)
+    k.lo = pos - a.window + 1 < held ? (int)(pos - a.window + 1) : held;
   if (pos < 0 || k.hi < 0) k.hi = 0;
   return k;
 }
@@ -93,21 +95,26 @@ __device__ __forceinline__ Keys keys_of(const AttendArgs& a, int64_t pos, int64_
 // What the rows [row_a, row_b) of a (sequence, head) see together, as pieces
 // of a.piece tokens from a 64-aligned start.
 struct Span {
-  int64_t lo, hi;  // lo a multiple of 64; lo >= hi: no key
+  int lo, hi;  // lo a multiple of 64; lo >= hi: no key
   int pieces;
 };
-__device__ __forceinline__ Span span_of(const AttendArgs& a, const SeqSpan& sp, int64_t held,
+__device__ __forceinline__ Span span_of(const AttendArgs& a, const SeqSpan& sp, int held,
                                         int tok_a, int tok_b) {
   Span r;
   const Keys f = keys_of(a, sp.start + tok_a, held), l = keys_of(a, sp.start + tok_b, held);
-  r.lo = f.lo & ~(int64_t)63;
+  r.lo = f.lo & ~63;
   r.hi = l.hi;
-  r.pieces = r.hi > r.lo ? (int)((r.hi - r.lo + a.piece - 1) / a.piece) : 0;
+  r.pieces = r.hi > r.lo ? (r.hi - r.lo + a.piece - 1) / a.piece : 0;
   return r;
 }
-__device__ __forceinline__ int64_t held_of(const AttendArgs& a, int s) {
-  const int64_t len = a.batch.kv_len[s];
-  const int64_t room = (int64_t)a.batch.table_pages * a.cache.block;
+// row / group: rows are below 2^26 and groups at most 2^10, so a product with
+// ceil(2^36 / group) is off by less than 1 / group of a unit.
+__device__ __forceinline__ int token_of(const AttendArgs& a, int row) {
+  return (int)(((uint64_t)(uint32_t)row * a.group_mul) >> 36);
+}
+__device__ __forceinline__ int held_of(const AttendArgs& a, int s) {
+  const int len = a.batch.kv_len[s];
+  const int room = a.batch.table_pages * a.cache.block;
   return len < room ? len : room;
 }
 
@@ -128,28 +135,82 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
   const int s = blockIdx.z;
   const int kvh = blockIdx.x % a.cache.heads;
   const int row_tile = blockIdx.x / a.cache.heads;
+  const int piece = blockIdx.y;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int g = lane >> 4, r16 = lane & 15;
+
+  // The pages are known one tile ahead of the codes, and a tile's codes are
+  // loaded as soon as the registers of the one before are free: k's after the
+  // first product, v's after the second.  Table entries are loaded without
+  // waiting for the lengths (without a window a piece's first key does not
+  // depend on them) and judged when both are there.
+  const int block = a.cache.block;
+  const int shift = __builtin_ctz(block);
+  const int* const table = a.batch.page_table + (int64_t)s * a.batch.table_pages;
+  // table entries of the 16 keys whose k this lane loads, and of its scores and v
+  int pk = -1, pv = -1;
+  auto pages = [&](int key0) {
+    const int ik = (key0 + 16 * (r16 >> 2)) >> shift, iv = (key0 + 16 * g) >> shift;
+    pk = ik < a.batch.table_pages ? table[ik] : -1;
+    pv = iv < a.batch.table_pages ? table[iv] : -1;
+  };
+  if (a.window == 0) pages(piece * a.piece + 64 * wave);
+
   const SeqSpan sp = seq_span(a.batch, s);
   const int rows = sp.n * a.group;  // rows of this sequence and head
   const int row_base = row_tile * (ROWS * 16);
   if (row_base >= rows) return;
   const int row_last = row_base + ROWS * 16 < rows ? row_base + ROWS * 16 - 1 : rows - 1;
-  const int64_t held = held_of(a, s);
-  const Span span = span_of(a, sp, held, row_base / a.group, row_last / a.group);
-  const int piece = blockIdx.y;
+  const int held = held_of(a, s);
+  const Span span = span_of(a, sp, held, token_of(a, row_base), token_of(a, row_last));
   if (piece > 0 && piece >= span.pieces) return;
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int g = lane >> 4, r16 = lane & 15;
+  const int begin = span.lo + piece * a.piece;
+  const int stop = begin + a.piece < span.hi ? begin + a.piece : span.hi;
+  const int head_bytes = block * DIM;
+  const int64_t page_bytes = (int64_t)head_bytes * a.cache.heads;
+  const uint8_t* const kbase = a.cache.k + (int64_t)kvh * head_bytes + (r16 & 3) * DIM + 16 * g;
+  const uint8_t* const vbase = a.cache.v + (int64_t)kvh * head_bytes + r16 * block;
+  u32x4 kc[4][C], vc[DT];
+  float ks, vs;
+  // entries of keys beyond the piece, or outside the pool, are no pages
+  auto judge = [&](int key0) {
+    if (key0 + 16 * (r16 >> 2) >= stop || pk >= a.cache.pages) pk = -1;
+    if (key0 + 16 * g >= stop || pv >= a.cache.pages) pv = -1;
+  };
+  auto load_k = [&](int key0) {
+    const uint8_t* p = kbase + (pk < 0 ? 0 : pk) * page_bytes +
+                       ((key0 + 16 * (r16 >> 2)) & (block - 1)) * DIM;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        kc[t][c] = *reinterpret_cast<const u32x4*>(p + 4 * t * DIM + 64 * c);
+    ks = a.cache.k_scale[(int64_t)(pv < 0 ? 0 : pv) * a.cache.heads + kvh];
+  };
+  auto load_v = [&](int key0) {
+    const uint8_t* p = vbase + (pv < 0 ? 0 : pv) * page_bytes + ((key0 + 16 * g) & (block - 1));
+#pragma unroll
+    for (int d = 0; d < DT; ++d) vc[d] = *reinterpret_cast<const u32x4*>(p + 16 * d * block);
+    vs = a.cache.v_scale[(int64_t)(pv < 0 ? 0 : pv) * a.cache.heads + kvh];
+  };
+  const int first_key = begin + 64 * wave;
+  if (first_key < stop) {
+    if (a.window != 0) pages(first_key);
+    judge(first_key);
+    load_k(first_key);
+    load_v(first_key);
+  }
 
   // ---- this lane's rows: the queries as fp16, and the keys they see
   f16x8 q[ROWS][C][2];
   float qf[ROWS];
-  int64_t see_lo[ROWS], see_hi[ROWS];
+  int see_lo[ROWS], see_hi[ROWS];
 #pragma unroll
   for (int rt = 0; rt < ROWS; ++rt) {
     const int row = row_base + rt * 16 + r16;
     const bool real = row < rows;
-    const int tok = real ? row / a.group : 0;
+    const int tok = real ? token_of(a, row) : 0;
     const int head = kvh * a.group + (real ? row - tok * a.group : 0);
     const uint16_t* qp = a.q + (int64_t)(sp.row0 + tok) * a.q_stride + (int64_t)head * DIM;
     u32x4 raw[C][2];
@@ -190,8 +251,8 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
     see_hi[rt] = real ? k.hi : 0;
   }
   // keys that every real row sees: no mask needed there
-  const Keys first = keys_of(a, sp.start + row_base / a.group, held);
-  const Keys last = keys_of(a, sp.start + row_last / a.group, held);
+  const Keys first = keys_of(a, sp.start + token_of(a, row_base), held);
+  const Keys last = keys_of(a, sp.start + token_of(a, row_last), held);
 
   f32x4 acc[ROWS][DT];
   float ref[ROWS], sum[ROWS];
@@ -204,61 +265,47 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
   }
   float vref = 0.f, vinv = 0.f;  // unit of the v scales in acc
 
-  const int64_t begin = span.lo + (int64_t)piece * a.piece;
-  const int64_t stop = begin + a.piece < span.hi ? begin + a.piece : span.hi;
-  const int block = a.cache.block;
-  const int shift = __builtin_ctz(block);
-  const int64_t page_bytes = (int64_t)block * DIM;
-  const float log_scale = kLog2e;
-
-  for (int64_t key0 = begin + 64 * wave; key0 < stop; key0 += 64 * NW) {
-    // pages of the 16 keys whose v this lane loads (and whose scores it gets),
-    // and of the keys whose k it loads
-    const int64_t kv0 = key0 + 16 * g, kk0 = key0 + 16 * (r16 >> 2);
-    const int pv = kv0 < stop ? page_of(a.batch, s, kv0 >> shift, a.cache.pages) : -1;
-    const int pk = kk0 < stop ? page_of(a.batch, s, kk0 >> shift, a.cache.pages) : -1;
-    const bool masked = key0 < last.lo || key0 + 64 > first.hi || key0 + 64 > stop ||
-                        __any(pv < 0);
-    const int64_t phv = (int64_t)(pv < 0 ? 0 : pv) * a.cache.heads + kvh;
-    const int64_t phk = (int64_t)(pk < 0 ? 0 : pk) * a.cache.heads + kvh;
-    const uint8_t* kp = a.cache.k + phk * page_bytes +
-                        ((kk0 & (block - 1)) + (r16 & 3)) * DIM + 16 * g;
-    const uint8_t* vp = a.cache.v + phv * page_bytes + (int64_t)r16 * block + (kv0 & (block - 1));
-    const float ks = a.cache.k_scale[phv];
-    float vs = a.cache.v_scale[phv];
-    u32x4 kc[4][C], vc[DT];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        kc[t][c] = *reinterpret_cast<const u32x4*>(kp + 4 * t * DIM + 64 * c);
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-      vc[d] = *reinterpret_cast<const u32x4*>(vp + (int64_t)16 * d * block);
+  const float icap = CAP ? 1.f / a.softcap : 0.f;
+  for (int key0 = first_key; key0 < stop; key0 += 64 * NW) {
+    const int kv0 = key0 + 16 * g;
+    const bool here = pv >= 0;
+    const bool masked =
+        key0 < last.lo || key0 + 64 > first.hi || key0 + 64 > stop || __any(!here);
+    const int next = key0 + 64 * NW;
+    const bool more = next < stop;
+    if (more) pages(next);
 
     // ---- scores
     f32x4 sc[ROWS][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int rt = 0; rt < ROWS; ++rt) sc[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        f16x8 lo, hi;
-        codes_to_f16<E4M3>(kc[t][c], &lo, &hi);
+    for (int c = 0; c < C; ++c) {
+      f16x8 op[4][2];
 #pragma unroll
-        for (int rt = 0; rt < ROWS; ++rt) {
-          sc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, q[rt][c][0], sc[rt][t], 0, 0, 0);
-          sc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, q[rt][c][1], sc[rt][t], 0, 0, 0);
-        }
-      }
+      for (int t = 0; t < 4; ++t) codes_to_f16<E4M3>(kc[t][c], &op[t][0], &op[t][1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int rt = 0; rt < ROWS; ++rt)
+            sc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op[t][h], q[rt][c][h], sc[rt][t], 0,
+                                                               0, 0);
+    }
+    const float ks_now = ks;
+    if (more) {
+      judge(next);
+      load_k(next);
     }
     // ---- mask: keys beyond the sequence, and bytes there (never written)
     // must not reach the products as NaN
     int live = 16;  // of this lane's 16 keys, those that are held
     if (masked) {
-      const int64_t n = stop - kv0;
-      live = pv < 0 || n <= 0 ? 0 : (n < 16 ? (int)n : 16);
+      const int n = stop - kv0;
+      live = !here || n <= 0 ? 0 : (n < 16 ? n : 16);
       if (live == 0) vs = 0.f;
     }
     // ---- unit of v
@@ -280,7 +327,7 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
     f16x8 p[ROWS][2];
 #pragma unroll
     for (int rt = 0; rt < ROWS; ++rt) {
-      const float f = CAP ? ks * qf[rt] : ks * qf[rt] * log_scale;
+      const float f = ks_now * qf[rt] * (CAP ? icap : kLog2e);
       float x[16];
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -288,14 +335,14 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
         for (int i = 0; i < 4; ++i) {
           float y = sc[rt][t][i] * f;
           if (CAP) {
-            y = capped(y / a.softcap) * (a.softcap * kLog2e);
+            y = capped(y) * (a.softcap * kLog2e);
           }
           x[4 * t + i] = y;
         }
       if (masked) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int64_t j = kv0 + i;
+          const int j = kv0 + i;
           if (i >= live || j < see_lo[rt] || j >= see_hi[rt]) x[i] = -INFINITY;
         }
       }
@@ -330,15 +377,20 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
     }
     // ---- O^T += V^T P^T
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      f16x8 lo, hi;
-      codes_to_f16<E4M3>(vc[d], &lo, &hi);
+    for (int d = 0; d < DT; d += 2) {
+      f16x8 op[2][2];
 #pragma unroll
-      for (int rt = 0; rt < ROWS; ++rt) {
-        acc[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, p[rt][0], acc[rt][d], 0, 0, 0);
-        acc[rt][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, p[rt][1], acc[rt][d], 0, 0, 0);
-      }
+      for (int e = 0; e < 2; ++e) codes_to_f16<E4M3>(vc[d + e], &op[e][0], &op[e][1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int rt = 0; rt < ROWS; ++rt)
+            acc[rt][d + e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op[e][h], p[rt][h],
+                                                                    acc[rt][d + e], 0, 0, 0);
     }
+    if (more) load_v(next);
   }
 
   // ---- join the waves: reference and sum of every row, then the outputs
@@ -384,7 +436,7 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
 #pragma unroll
       for (int w = 0; w < NW; ++w)
         ll += lds_ml[w][rt * 16 + rr][1] * __builtin_amdgcn_exp2f(lds_ml[w][rt * 16 + rr][0] - mm);
-      const int tok = row / a.group;
+      const int tok = token_of(a, row);
       const int64_t out_row =
           (int64_t)(sp.row0 + tok) * a.q_heads + kvh * a.group + (row - tok * a.group);
       if (direct) {
@@ -447,8 +499,8 @@ attend_many_kernel(AttendArgs a) {
   if (row_tile < 0) return;
   const int row_base = row_tile * (NW * 32);
   const int row_last = row_base + NW * 32 < rows ? row_base + NW * 32 - 1 : rows - 1;
-  const int64_t held = held_of(a, s);
-  const Span span = span_of(a, sp, held, row_base / a.group, row_last / a.group);
+  const int held = held_of(a, s);
+  const Span span = span_of(a, sp, held, token_of(a, row_base), token_of(a, row_last));
   const int piece = blockIdx.y;
   if (piece > 0 && piece >= span.pieces) return;
 
@@ -459,7 +511,7 @@ attend_many_kernel(AttendArgs a) {
   // ---- this lane's row
   const int row = row_base + wave * 32 + r32;
   const bool real = row < rows;
-  const int tok = real ? row / a.group : 0;
+  const int tok = real ? token_of(a, row) : 0;
   const int head = kvh * a.group + (real ? row - tok * a.group : 0);
   f16x8 q[KS];
   float qf;
@@ -499,13 +551,16 @@ attend_many_kernel(AttendArgs a) {
   const int wrow = row_base + wave * 32;
   const int wlast = wrow + 31 < rows ? wrow + 31 : rows - 1;
   const bool wreal = wrow < rows;
-  const Keys wf = keys_of(a, sp.start + (wreal ? wrow / a.group : 0), held);
-  const Keys wl = keys_of(a, sp.start + (wreal ? wlast / a.group : 0), held);
+  const Keys wf = keys_of(a, sp.start + (wreal ? token_of(a, wrow) : 0), held);
+  const Keys wl = keys_of(a, sp.start + (wreal ? token_of(a, wlast) : 0), held);
 
-  const int64_t begin = span.lo + (int64_t)piece * a.piece;
-  const int64_t stop = begin + a.piece < span.hi ? begin + a.piece : span.hi;
+  const int begin = span.lo + piece * a.piece;
+  const int stop = begin + a.piece < span.hi ? begin + a.piece : span.hi;
   const int block = a.cache.block, shift = __builtin_ctz(block);
-  const int64_t page_bytes = (int64_t)block * DIM;
+  const int head_bytes = block * DIM;
+  const int64_t page_bytes = (int64_t)head_bytes * a.cache.heads;
+  const uint8_t* const kbase = a.cache.k + (int64_t)kvh * head_bytes;
+  const uint8_t* const vbase = a.cache.v + (int64_t)kvh * head_bytes;
 
   f32x16 acc[DT];
 #pragma unroll
@@ -515,39 +570,30 @@ attend_many_kernel(AttendArgs a) {
   // ---- staging: pages one tile further ahead than codes
   u32x4 kc[KC], vc[KC];
   float ksc[KC] = {}, vsc = 0.f;
-  int pk[KC], pv[KC], live0 = 0;
-  auto load_pages = [&](int64_t key0) {
+  int pk[KC], pv[KC], live[KC];
+  auto load_pages = [&](int key0) {
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int c = tid + i * T;
-      const int64_t kk = key0 + (c / KS & ~15), kv = key0 + (c & 3) * 16;
+      const int kk = key0 + (c / KS & ~15), kv = key0 + (c & 3) * 16;
       pk[i] = kk < stop ? page_of(a.batch, s, kk >> shift, a.cache.pages) : -1;
       pv[i] = kv < stop ? page_of(a.batch, s, kv >> shift, a.cache.pages) : -1;
     }
   };
-  auto load_codes = [&](int64_t key0) {
+  auto load_codes = [&](int key0) {
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int c = tid + i * T;
       const int key = c / KS, ks = c % KS, dim = c >> 2, kst = c & 3;
-      const int64_t hk = (int64_t)(pk[i] < 0 ? 0 : pk[i]) * a.cache.heads + kvh;
-      const int64_t hv = (int64_t)(pv[i] < 0 ? 0 : pv[i]) * a.cache.heads + kvh;
-      kc[i] = *reinterpret_cast<const u32x4*>(
-          a.cache.k + hk * page_bytes + (int64_t)((key0 + key) & (block - 1)) * DIM + 16 * ks);
-      vc[i] = *reinterpret_cast<const u32x4*>(a.cache.v + hv * page_bytes + (int64_t)dim * block +
-                                              ((key0 + 16 * kst) & (block - 1)));
-      const int64_t n = stop - (key0 + 16 * kst);
-      const int live = pv[i] < 0 || n <= 0 ? 0 : (n < 16 ? (int)n : 16);
-      if (live < 16) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int keep = live - 4 * e;
-          vc[i][e] &= keep >= 4 ? 0xffffffffu : (keep <= 0 ? 0u : (1u << (8 * keep)) - 1);
-        }
-      }
-      if (i == 0) live0 = live;
-      if (ks == 0 && (key & 15) == 0) ksc[i] = a.cache.k_scale[hk];
-      if (i == 0 && dim == 0) vsc = a.cache.v_scale[hv];
+      const int hk = pk[i] < 0 ? 0 : pk[i], hv = pv[i] < 0 ? 0 : pv[i];
+      kc[i] = *reinterpret_cast<const u32x4*>(kbase + hk * page_bytes +
+                                              (((key0 + key) & (block - 1)) * DIM + 16 * ks));
+      vc[i] = *reinterpret_cast<const u32x4*>(vbase + hv * page_bytes +
+                                              (dim * block + ((key0 + 16 * kst) & (block - 1))));
+      const int n = stop - (key0 + 16 * kst);
+      live[i] = pv[i] < 0 || n <= 0 ? 0 : (n < 16 ? n : 16);
+      if (ks == 0 && (key & 15) == 0) ksc[i] = a.cache.k_scale[(int64_t)hk * a.cache.heads + kvh];
+      if (i == 0 && dim == 0) vsc = a.cache.v_scale[(int64_t)hv * a.cache.heads + kvh];
     }
   };
   auto store_tile = [&](int buf) {
@@ -562,14 +608,21 @@ attend_many_kernel(AttendArgs a) {
       const int swk = KS == 4 ? 2 * ks : ks & 7;
       lds_k[buf][key >> 5][ks][m ^ swk] = __builtin_bit_cast(u32x4, lo);
       lds_k[buf][key >> 5][ks][(32 + m) ^ swk] = __builtin_bit_cast(u32x4, hi);
+      if (live[i] < 16) {  // bytes beyond the sequence must not become NaN
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int keep = live[i] - 4 * w;
+          vc[i][w] &= keep >= 4 ? 0xffffffffu : (keep <= 0 ? 0u : (1u << (8 * keep)) - 1);
+        }
+      }
       codes_to_f16<E4M3>(vc[i], &lo, &hi);
       const int swv = 2 * kst;
       lds_v[buf][kst][dim >> 5][(dim & 31) ^ swv] = __builtin_bit_cast(u32x4, lo);
       lds_v[buf][kst][dim >> 5][(32 + (dim & 31)) ^ swv] = __builtin_bit_cast(u32x4, hi);
       if (ks == 0 && (key & 15) == 0) lds_ks[buf][key >> 4] = ksc[i];
       if (i == 0 && dim == 0) {
-        lds_vs[buf][kst] = live0 > 0 ? vsc : 0.f;
-        lds_live[buf][kst] = live0;
+        lds_vs[buf][kst] = live[0] > 0 ? vsc : 0.f;
+        lds_live[buf][kst] = live[0];
       }
     }
   };
@@ -583,7 +636,7 @@ attend_many_kernel(AttendArgs a) {
     load_pages(begin + 128);
   }
   int buf = 0;
-  for (int64_t key0 = begin; key0 < stop; key0 += 64, buf ^= 1) {
+  for (int key0 = begin; key0 < stop; key0 += 64, buf ^= 1) {
     __syncthreads();
     if (key0 + 64 < stop) {
       store_tile(buf ^ 1);
@@ -645,7 +698,7 @@ attend_many_kernel(AttendArgs a) {
         const int live = lds_live[buf][e];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int64_t j = key0 + 16 * e + 8 * h + i;
+          const int j = key0 + 16 * e + 8 * h + i;
           if (8 * h + i >= live || j < see.lo || j >= see.hi)
             sc[e >> 1][8 * (e & 1) + i] = -INFINITY;
         }
@@ -731,44 +784,78 @@ attend_many_kernel(AttendArgs a) {
 
 // ------------------------------------------------------------- the join
 //
-// One wave a row: the pieces' references and sums, then their outputs.
+// One workgroup a row: 256 / (DIM / 4) groups of threads take the pieces in
+// turn, each with a reference, a sum and four outputs a thread of its own,
+// joined through LDS.
 template <int DIM>
 __global__ void __launch_bounds__(256) join_kernel(AttendArgs a, int tile_rows) {
-  constexpr int E = DIM / 64;
+  constexpr int L = DIM / 4, G = 256 / L;
+  __shared__ f32x4 lds_o[G][L];
+  __shared__ float lds_ml[G][2];
   const int s = blockIdx.z;
   const int kvh = blockIdx.y;
   const SeqSpan sp = seq_span(a.batch, s);
   const int rows = sp.n * a.group;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int row = blockIdx.x;
   if (row >= rows) return;
-  const int64_t held = held_of(a, s);
+  const int held = held_of(a, s);
   const int row_base = row / tile_rows * tile_rows;
   const int row_last = row_base + tile_rows < rows ? row_base + tile_rows - 1 : rows - 1;
-  const Span span = span_of(a, sp, held, row_base / a.group, row_last / a.group);
+  const Span span = span_of(a, sp, held, token_of(a, row_base), token_of(a, row_last));
   if (span.pieces <= 1) return;  // written already
-  const int lane = threadIdx.x & 63;
-  const int tok = row / a.group;
+  const int l = threadIdx.x % L, pg = threadIdx.x / L;
+  const int tok = token_of(a, row);
   const int64_t out_row =
       (int64_t)(sp.row0 + tok) * a.q_heads + kvh * a.group + (row - tok * a.group);
   const int64_t step = a.batch.rows * a.q_heads;
-  float m = kNoRef;
-  for (int i = lane; i < span.pieces; i += 64) m = fmaxf(m, a.part_ml[2 * (out_row + i * step)]);
-  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-  float l = 0.f, o[E];
+  float m = kNoRef, sum = 0.f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = pg; i0 < span.pieces; i0 += 4 * G) {
+    float mi[4], si[4];
+    f32x4 oi[4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int i = 0; i < span.pieces; ++i) {
-    const int64_t at = out_row + i * step;
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - m);
-    l += a.part_ml[2 * at + 1] * f;
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * G;
+      const int64_t at = out_row + (i < span.pieces ? i : i0) * step;
+      mi[j] = a.part_ml[2 * at];
+      si[j] = a.part_ml[2 * at + 1];
+      oi[j] = *reinterpret_cast<const f32x4*>(a.part_o + at * DIM + 4 * l);
+    }
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += a.part_o[at * DIM + lane * E + e] * f;
+    for (int j = 0; j < 4; ++j) {
+      if (i0 + j * G >= span.pieces) continue;
+      const float top = fmaxf(m, mi[j]);
+      const float f = __builtin_amdgcn_exp2f(m - top), fi = __builtin_amdgcn_exp2f(mi[j] - top);
+      sum = sum * f + si[j] * fi;
+      o = o * f + oi[j] * fi;
+      m = top;
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (l == 0) {
+    lds_ml[pg][0] = m;
+    lds_ml[pg][1] = sum;
+  }
+  lds_o[pg][l] = o;
+  __syncthreads();
+  if (pg != 0) return;
+  float top = kNoRef;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    a.out[out_row * DIM + lane * E + e] = l == 0.f ? 0 : (uint16_t)bf16_rne(o[e] * inv);
-  if (a.lse && lane == 0) a.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  for (int i = 0; i < G; ++i) top = fmaxf(top, lds_ml[i][0]);
+  sum = 0.f;
+  o = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const float f = __builtin_amdgcn_exp2f(lds_ml[i][0] - top);
+    sum += lds_ml[i][1] * f;
+    o = o + lds_o[i][l] * f;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  u32x2 b;
+  b[0] = bf16_rne(o[0] * inv) | (bf16_rne(o[1] * inv) << 16);
+  b[1] = bf16_rne(o[2] * inv) | (bf16_rne(o[3] * inv) << 16);
+  if (sum == 0.f) b = u32x2{0, 0};
+  *reinterpret_cast<u32x2*>(a.out + out_row * DIM + 4 * l) = b;
+  if (a.lse && l == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 namespace {
@@ -829,7 +916,7 @@ hipError_t attend_dim(AttendArgs& a, hipStream_t s) {
                  : tile == 32 ? few<DIM, 2, kFewWaves>(a, grid, s)
                               : many<DIM>(a, grid, s);
   if (e != hipSuccess || a.pieces <= 1) return e;
-  const dim3 jg((unsigned)((most + 3) / 4), (unsigned)a.cache.heads, (unsigned)a.batch.seqs);
+  const dim3 jg((unsigned)most, (unsigned)a.cache.heads, (unsigned)a.batch.seqs);
   hipLaunchKernelGGL((join_kernel<DIM>), jg, dim3(256), 0, s, a, tile);
   return hipGetLastError();
 }
@@ -843,10 +930,14 @@ size_t attend_plan(AttendArgs& a) {
   if (a.window > 0 && a.window + a.batch.max_new + 64 < keys)
     keys = a.window + a.batch.max_new + 64;
   const int64_t groups = (int64_t)a.batch.seqs * a.cache.heads * ((most + tile - 1) / tile);
-  int64_t pieces = 2048 / groups;
-  if (pieces < 1) pieces = 1;
+  // Two workgroups a CU; with several sequences, whose lengths the host does
+  // not know, at least 16 pieces of the longest possible one, so that long
+  // sequences do not run on behind short ones; and 512 tokens a piece where
+  // that still fills the chip, 256 (one tile a wave) where it does not.
+  int64_t pieces = (512 + groups - 1) / groups;
+  if (tile <= 32 && a.batch.seqs > 1 && pieces < 16) pieces = 16;
   int64_t piece = (keys + pieces - 1) / pieces;
-  const int64_t least = 64 * kFewWaves;
+  const int64_t least = groups * keys >= 512 * 256 ? 512 : 64 * kFewWaves;
   piece = (piece + least - 1) / least * least;
   a.piece = (int)piece;
   a.pieces = (int)((keys + piece - 1) / piece);

@@ -156,6 +156,7 @@ struct AttendArgs {
   const uint16_t* q;
   int64_t q_stride;
   int group, q_heads;
+  uint64_t group_mul;  // ceil(2^36 / group)
   float scale, softcap;
   int64_t window;
   int causal;
