@@ -37,26 +37,24 @@ constexpr float kNoRef = -1e30f;  // reference of a row that has seen no key
 // exchange between lanes and no rescaling.
 constexpr float kSlack = 8.f;
 
-// 16 codes (as loaded) to two operands of eight fp16.
+// Eight codes to an operand of eight fp16.
 template <bool E4M3>
-__device__ __forceinline__ void codes_to_f16(u32x4 w, f16x8* a, f16x8* b) {
+__device__ __forceinline__ f16x8 codes_to_f16(uint32_t w0, uint32_t w1) {
   union {
-    f16x2 h[8];
-    f16x8 v[2];
+    f16x2 h[4];
+    f16x8 v;
   } r;
-  if (E4M3) {
+  const uint32_t w[2] = {w0, w1};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
+    if (E4M3) {
       r.h[2 * i] = __builtin_bit_cast(
           f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w[i], 1.f, false));
       r.h[2 * i + 1] = __builtin_bit_cast(
           f16x2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w[i], 1.f, true));
-    }
-  } else {
-    // byte c + 128 under the fp16 exponent of 1024 is 1152 + c
-    const f16x2 off = {(_Float16)1152.f, (_Float16)1152.f};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    } else {
+      // byte c + 128 under the fp16 exponent of 1024 is 1152 + c
+      const f16x2 off = {(_Float16)1152.f, (_Float16)1152.f};
       const uint32_t u = w[i] ^ 0x80808080u;
       const uint32_t p0 = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
       const uint32_t p1 = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
@@ -64,8 +62,7 @@ __device__ __forceinline__ void codes_to_f16(u32x4 w, f16x8* a, f16x8* b) {
       r.h[2 * i + 1] = __builtin_bit_cast(f16x2, p1) - off;
     }
   }
-  *a = r.v[0];
-  *b = r.v[1];
+  return r.v;
 }
 
 // tanh(z) = 1 - 2 / (e^2z + 1), by its series where that cancels (cut below
@@ -125,10 +122,19 @@ __device__ __forceinline__ int held_of(const AttendArgs& a, int s) {
 // ROWS * 16 rows a workgroup, NW waves that share them and take the piece's
 // 64-key tiles in turn, each with sums of its own, joined through LDS at the
 // end; pieces are joined by join_kernel.  Bound by the codes' bytes.
-template <int DIM, int ROWS, int NW, bool E4M3, bool CAP>
-__global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
+// Waves of a SIMD that the registers are cut for (k and v of a tile, the
+// outputs, the queries).
+constexpr int few_waves(int dim, int rows, int kt) {
+  return dim * (rows + kt / 32) <= 256 ? 3 : dim * (rows + kt / 32) <= 512 ? 2 : 1;
+}
+
+template <int DIM, int ROWS, int KT, int NW, bool E4M3, bool CAP>
+__global__ void __launch_bounds__(NW * 64)
+    __attribute__((amdgpu_waves_per_eu(few_waves(DIM, ROWS, KT)))) attend_few_kernel(AttendArgs a) {
   constexpr int C = DIM / 64;   // 64-dim chunks of a key
   constexpr int DT = DIM / 16;  // 16-dim tiles of the output
+  constexpr int NT = KT / 16;   // 16-key products of a tile
+  constexpr int KL = KT / 4;    // consecutive keys of a lane: 16 or 8
   __shared__ float lds_o[NW][16][DIM + 4];
   __shared__ float lds_ml[NW][ROWS * 16][2];
 
@@ -150,11 +156,11 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
   // table entries of the 16 keys whose k this lane loads, and of its scores and v
   int pk = -1, pv = -1;
   auto pages = [&](int key0) {
-    const int ik = (key0 + 16 * (r16 >> 2)) >> shift, iv = (key0 + 16 * g) >> shift;
+    const int ik = (key0 + KL * (r16 >> 2)) >> shift, iv = (key0 + KL * g) >> shift;
     pk = ik < a.batch.table_pages ? table[ik] : -1;
     pv = iv < a.batch.table_pages ? table[iv] : -1;
   };
-  if (a.window == 0) pages(piece * a.piece + 64 * wave);
+  if (a.window == 0) pages(piece * a.piece + KT * wave);
 
   const SeqSpan sp = seq_span(a.batch, s);
   const int rows = sp.n * a.group;  // rows of this sequence and head
@@ -171,30 +177,39 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
   const int64_t page_bytes = (int64_t)head_bytes * a.cache.heads;
   const uint8_t* const kbase = a.cache.k + (int64_t)kvh * head_bytes + (r16 & 3) * DIM + 16 * g;
   const uint8_t* const vbase = a.cache.v + (int64_t)kvh * head_bytes + r16 * block;
-  u32x4 kc[4][C], vc[DT];
+  u32x4 kc[NT][C];
+  uint32_t vc[DT][KL / 4];
   float ks, vs;
   // entries of keys beyond the piece, or outside the pool, are no pages
   auto judge = [&](int key0) {
-    if (key0 + 16 * (r16 >> 2) >= stop || pk >= a.cache.pages) pk = -1;
-    if (key0 + 16 * g >= stop || pv >= a.cache.pages) pv = -1;
+    if (key0 + KL * (r16 >> 2) >= stop || pk >= a.cache.pages) pk = -1;
+    if (key0 + KL * g >= stop || pv >= a.cache.pages) pv = -1;
   };
   auto load_k = [&](int key0) {
     const uint8_t* p = kbase + (pk < 0 ? 0 : pk) * page_bytes +
-                       ((key0 + 16 * (r16 >> 2)) & (block - 1)) * DIM;
+                       ((key0 + KL * (r16 >> 2)) & (block - 1)) * DIM;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int c = 0; c < C; ++c)
         kc[t][c] = *reinterpret_cast<const u32x4*>(p + 4 * t * DIM + 64 * c);
     ks = a.cache.k_scale[(int64_t)(pv < 0 ? 0 : pv) * a.cache.heads + kvh];
   };
   auto load_v = [&](int key0) {
-    const uint8_t* p = vbase + (pv < 0 ? 0 : pv) * page_bytes + ((key0 + 16 * g) & (block - 1));
+    const uint8_t* p = vbase + (pv < 0 ? 0 : pv) * page_bytes + ((key0 + KL * g) & (block - 1));
 #pragma unroll
-    for (int d = 0; d < DT; ++d) vc[d] = *reinterpret_cast<const u32x4*>(p + 16 * d * block);
+    for (int d = 0; d < DT; ++d) {
+      if (KL == 16) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p + 16 * d * block);
+        vc[d][0] = w[0], vc[d][1] = w[1], vc[d][KL / 4 - 2] = w[2], vc[d][KL / 4 - 1] = w[3];
+      } else {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p + 16 * d * block);
+        vc[d][0] = w[0], vc[d][1] = w[1];
+      }
+    }
     vs = a.cache.v_scale[(int64_t)(pv < 0 ? 0 : pv) * a.cache.heads + kvh];
   };
-  const int first_key = begin + 64 * wave;
+  const int first_key = begin + KT * wave;
   if (first_key < stop) {
     if (a.window != 0) pages(first_key);
     judge(first_key);
@@ -266,30 +281,33 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
   float vref = 0.f, vinv = 0.f;  // unit of the v scales in acc
 
   const float icap = CAP ? 1.f / a.softcap : 0.f;
-  for (int key0 = first_key; key0 < stop; key0 += 64 * NW) {
-    const int kv0 = key0 + 16 * g;
+  for (int key0 = first_key; key0 < stop; key0 += KT * NW) {
+    const int kv0 = key0 + KL * g;
     const bool here = pv >= 0;
     const bool masked =
-        key0 < last.lo || key0 + 64 > first.hi || key0 + 64 > stop || __any(!here);
-    const int next = key0 + 64 * NW;
+        key0 < last.lo || key0 + KT > first.hi || key0 + KT > stop || __any(!here);
+    const int next = key0 + KT * NW;
     const bool more = next < stop;
     if (more) pages(next);
 
     // ---- scores
-    f32x4 sc[ROWS][4];
+    f32x4 sc[ROWS][NT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int rt = 0; rt < ROWS; ++rt) sc[rt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      f16x8 op[4][2];
+      f16x8 op[NT][2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) codes_to_f16<E4M3>(kc[t][c], &op[t][0], &op[t][1]);
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          op[t][h] = codes_to_f16<E4M3>(kc[t][c][2 * h], kc[t][c][2 * h + 1]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int rt = 0; rt < ROWS; ++rt)
             sc[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(op[t][h], q[rt][c][h], sc[rt][t], 0,
@@ -302,10 +320,10 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
     }
     // ---- mask: keys beyond the sequence, and bytes there (never written)
     // must not reach the products as NaN
-    int live = 16;  // of this lane's 16 keys, those that are held
+    int live = KL;  // of this lane's keys, those that are held
     if (masked) {
       const int n = stop - kv0;
-      live = !here || n <= 0 ? 0 : (n < 16 ? n : 16);
+      live = !here || n <= 0 ? 0 : (n < KL ? n : KL);
       if (live == 0) vs = 0.f;
     }
     // ---- unit of v
@@ -324,13 +342,13 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
     }
     const float vw = vs * vinv;
     // ---- probabilities
-    f16x8 p[ROWS][2];
+    f16x8 p[ROWS][KT / 32];
 #pragma unroll
     for (int rt = 0; rt < ROWS; ++rt) {
       const float f = ks_now * qf[rt] * (CAP ? icap : kLog2e);
-      float x[16];
+      float x[KL];
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float y = sc[rt][t][i] * f;
@@ -341,14 +359,14 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
         }
       if (masked) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < KL; ++i) {
           const int j = kv0 + i;
           if (i >= live || j < see_lo[rt] || j >= see_hi[rt]) x[i] = -INFINITY;
         }
       }
       float top = x[0];
 #pragma unroll
-      for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
+      for (int i = 1; i < KL; ++i) top = fmaxf(top, x[i]);
       if (__any(top > ref[rt] + kSlack)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -360,7 +378,7 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
         for (int d = 0; d < DT; ++d) acc[rt][d] = acc[rt][d] * f2;
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < KL; ++i) {
         const float e = __builtin_amdgcn_exp2f(x[i] - ref[rt]);
         sum[rt] += e;
         p[rt][i >> 3][i & 7] = (_Float16)(e * vw);
@@ -370,7 +388,7 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < KL / 4; ++e) {
           const int keep = live - 4 * e;
           vc[d][e] &= keep >= 4 ? 0xffffffffu : (keep <= 0 ? 0u : (1u << (8 * keep)) - 1);
         }
@@ -378,11 +396,14 @@ __global__ void __launch_bounds__(NW * 64) attend_few_kernel(AttendArgs a) {
     // ---- O^T += V^T P^T
 #pragma unroll
     for (int d = 0; d < DT; d += 2) {
-      f16x8 op[2][2];
+      f16x8 op[2][KT / 32];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) codes_to_f16<E4M3>(vc[d + e], &op[e][0], &op[e][1]);
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < KT / 32; ++h)
+          op[e][h] = codes_to_f16<E4M3>(vc[d + e][2 * h], vc[d + e][2 * h + 1]);
+#pragma unroll
+      for (int h = 0; h < KT / 32; ++h)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -601,8 +622,8 @@ attend_many_kernel(AttendArgs a) {
     for (int i = 0; i < KC; ++i) {
       const int c = tid + i * T;
       const int key = c / KS, ks = c % KS, dim = c >> 2, kst = c & 3;
-      f16x8 lo, hi;
-      codes_to_f16<E4M3>(kc[i], &lo, &hi);
+      f16x8 lo = codes_to_f16<E4M3>(kc[i][0], kc[i][1]);
+      f16x8 hi = codes_to_f16<E4M3>(kc[i][2], kc[i][3]);
       // row of the S^T product that gives this key: see above
       const int e = key & 15, m = (key & 16) | ((e & 8) >> 1) | ((e & 4) << 1) | (e & 3);
       const int swk = KS == 4 ? 2 * ks : ks & 7;
@@ -615,7 +636,8 @@ attend_many_kernel(AttendArgs a) {
           vc[i][w] &= keep >= 4 ? 0xffffffffu : (keep <= 0 ? 0u : (1u << (8 * keep)) - 1);
         }
       }
-      codes_to_f16<E4M3>(vc[i], &lo, &hi);
+      lo = codes_to_f16<E4M3>(vc[i][0], vc[i][1]);
+      hi = codes_to_f16<E4M3>(vc[i][2], vc[i][3]);
       const int swv = 2 * kst;
       lds_v[buf][kst][dim >> 5][(dim & 31) ^ swv] = __builtin_bit_cast(u32x4, lo);
       lds_v[buf][kst][dim >> 5][(32 + (dim & 31)) ^ swv] = __builtin_bit_cast(u32x4, hi);
@@ -869,20 +891,27 @@ int rows_tile(int64_t most_rows, int dim) {
 }
 constexpr int kFewWaves = 4;
 
+// Keys of a wave's tile: 32 leave dim 256 two waves a SIMD (16 sequences of 8192 tokens:
+// 68 -> 55 us, eight sequences of five drafted tokens 34 -> 24 us) and dim 64 four (10.2 ->
+// 9.6 us); at dim 128 64 keys keep two waves and more bytes in flight (32 sequences: 103
+// against 107 us).
+constexpr int few_keys(int dim) { return dim == 128 ? 64 : 32; }
+
 template <int DIM, int ROWS, int NW>
 hipError_t few(const AttendArgs& a, dim3 grid, hipStream_t s) {
+  constexpr int KT = few_keys(DIM);
   const dim3 block(NW * 64);
   const bool cap = a.softcap > 0.f;
   if (a.cache.e4m3) {
     if (cap)
-      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, NW, true, true>), grid, block, 0, s, a);
+      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, KT, NW, true, true>), grid, block, 0, s, a);
     else
-      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, NW, true, false>), grid, block, 0, s, a);
+      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, KT, NW, true, false>), grid, block, 0, s, a);
   } else {
     if (cap)
-      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, NW, false, true>), grid, block, 0, s, a);
+      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, KT, NW, false, true>), grid, block, 0, s, a);
     else
-      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, NW, false, false>), grid, block, 0, s, a);
+      hipLaunchKernelGGL((attend_few_kernel<DIM, ROWS, KT, NW, false, false>), grid, block, 0, s, a);
   }
   return hipGetLastError();
 }
