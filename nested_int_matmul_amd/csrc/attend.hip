@@ -484,22 +484,30 @@ __global__ void __launch_bounds__(NW * 64)
 //
 // NW waves of 32 rows each (32x32x16 products), one 64-key tile after the
 // other for all of them.  The tile's codes are converted to fp16 once for the
-// workgroup and staged through LDS as operand fragments (two buffers, one
-// barrier a tile); a lane's fragment is 16 consecutive bytes, and fragments
-// are permuted within groups of eight lanes (an XOR with the fragment's
-// index) so that both the staging stores and the operand loads touch all
-// banks evenly.  The 32 key rows of an S^T product are ordered so that a lane
-// (row lane % 32, half h = lane / 32) gets keys 16 e + 8 h + 0..7 of the tile
-// in registers 8 e .. 8 e + 7: eight consecutive keys of one 16-key group, the
-// operand of the second product as it stands.  A 16-key group lies in one
-// page, so its scales are the same for all lanes.
+// workgroup and staged through LDS as operand fragments (two buffers each for
+// k and v, one barrier a tile); a lane's fragment is 16 consecutive bytes, and
+// fragments are permuted within groups of eight lanes (an XOR with the
+// fragment's index) so that both the staging stores and the operand loads
+// touch all banks evenly.  The 32 key rows of an S^T product are ordered so
+// that a lane (row lane % 32, half h = lane / 32) gets keys 16 e + 8 h + 0..7
+// of the tile in registers 8 e .. 8 e + 7: eight consecutive keys of one
+// 16-key group, the operand of the second product as it stands.  A 16-key
+// group lies in one page, so its scales are the same for all lanes.
 //
-// The v scale of a group goes into the exponent: p = exp2(t - ref + log2 w),
-// w = v_scale / (largest v_scale so far), which saves a multiplication a
-// probability; the row's sum takes (sum of the group's p) / w.
+// What bounds it is the vector unit beside the matrix unit: an exp2 (four
+// issue slots), a multiply-add, an addition, half a maximum and half a
+// conversion a score, about as long as the two products take.  So the scores
+// of the next tile are computed while this tile's probabilities are (matrix
+// and vector instructions of one wave in the same stretch of code), and the
+// next codes are converted beside the second product.
+//
+// The v scale of a group goes into the exponent, p = exp2(t + log2 v_scale -
+// ref), so that probabilities need no further factor; the row's sum takes
+// (sum of the group's p) / v_scale.  A page of zeros (scale 0) is given the
+// scale of the page before it (2^-100 if there is none): any would do.
 template <int DIM, int NW, bool E4M3, bool CAP>
-__global__ void __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(DIM == 256 ? 1 : 2)))
-attend_many_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(NW * 64)
+    __attribute__((amdgpu_waves_per_eu(DIM == 256 ? 1 : 2))) attend_many_kernel(AttendArgs a) {
   constexpr int T = NW * 64;      // threads
   constexpr int KS = DIM / 16;    // 16-dim steps of the first product
   constexpr int DT = DIM / 32;    // 32-dim tiles of the output
@@ -507,7 +515,9 @@ attend_many_kernel(AttendArgs a) {
   static_assert(64 * KS % T == 0, "pieces");
   __shared__ u32x4 lds_k[2][2][KS][64];
   __shared__ u32x4 lds_v[2][4][DT][64];
-  __shared__ float lds_ks[2][4], lds_vs[2][4];
+  // of a tile's four 16-key groups: k scale, log2 and inverse of the v scale,
+  // v scale, keys held
+  __shared__ float lds_ks[2][4], lds_lv[2][4], lds_iv[2][4], lds_vs[2][4];
   __shared__ int lds_live[2][4];
 
   const int s = blockIdx.z;
@@ -557,7 +567,7 @@ attend_many_kernel(AttendArgs a) {
     // (a negative scale turns the queries round, so that factors are >= 0)
     const float up = copysignf(__uint_as_float((uint32_t)(14 - e + 127) << 23), a.scale);
     qf = __uint_as_float((uint32_t)(e - 14 + 127) << 23) * fabsf(a.scale);
-    if (!CAP) qf *= kLog2e;
+    qf *= CAP ? 1.f / a.softcap : kLog2e;
 #pragma unroll
     for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -577,142 +587,223 @@ attend_many_kernel(AttendArgs a) {
 
   const int begin = span.lo + piece * a.piece;
   const int stop = begin + a.piece < span.hi ? begin + a.piece : span.hi;
+  const int n_tiles = stop > begin ? (stop - begin + 63) >> 6 : 0;
   const int block = a.cache.block, shift = __builtin_ctz(block);
   const int head_bytes = block * DIM;
-  const int64_t page_bytes = (int64_t)head_bytes * a.cache.heads;
+  const uint32_t page_bytes = (uint32_t)head_bytes * a.cache.heads;
   const uint8_t* const kbase = a.cache.k + (int64_t)kvh * head_bytes;
   const uint8_t* const vbase = a.cache.v + (int64_t)kvh * head_bytes;
+  const int* const table = a.batch.page_table + (int64_t)s * a.batch.table_pages;
 
   f32x16 acc[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) acc[d] = f32x16{};
-  float ref = kNoRef, sum = 0.f, vref = 0.f;
+  float ref = kNoRef, sum = 0.f, vlast = kMinScale;
 
-  // ---- staging: pages one tile further ahead than codes
+  // ---- staging.  Thread tid converts k's piece (key c / KS, 16-dim step
+  // c % KS) and v's piece (dim c / 4, 16-key group c % 4), c = tid + i T; the
+  // 16-key group of its k is the same for the whole wave.
   u32x4 kc[KC], vc[KC];
-  float ksc[KC] = {}, vsc = 0.f;
-  int pk[KC], pv[KC], live[KC];
-  auto load_pages = [&](int key0) {
+  float ksc = 0.f, vsc = 0.f;
+  struct Pages {
+    int p[4];  // of a tile's 16-key groups, -1: none
+  };
+  // this tile's table entries, group lane % 4
+  auto entries = [&](int t) {
+    const int key = begin + 64 * t + 16 * (lane & 3);
+    int p = -1;
+    if (key < stop) p = table[key >> shift];
+    return p;
+  };
+  auto pages_of = [&](int v) {
+    Pages r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int p = __builtin_amdgcn_readlane(v, e);
+      r.p[e] = p < 0 || p >= a.cache.pages ? -1 : p;
+    }
+    return r;
+  };
+  auto group_of = [&](const Pages& p) {  // the entry of group tid % 4
+    const int x = (tid & 1) ? p.p[1] : p.p[0], y = (tid & 1) ? p.p[3] : p.p[2];
+    return (tid & 2) ? y : x;
+  };
+  auto load_k = [&](const Pages& p, int t) {
+    const int at = (begin + 64 * t) & (block - 1);
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int c = tid + i * T;
-      const int kk = key0 + (c / KS & ~15), kv = key0 + (c & 3) * 16;
-      pk[i] = kk < stop ? page_of(a.batch, s, kk >> shift, a.cache.pages) : -1;
-      pv[i] = kv < stop ? page_of(a.batch, s, kv >> shift, a.cache.pages) : -1;
+      // group of key c / KS: DIM 256: i; 128: wave / 2; 64: wave
+      const int e = DIM == 256 ? i : DIM == 128 ? wave >> 1 : wave;
+      const int x = (e & 1) ? p.p[1] : p.p[0], y = (e & 1) ? p.p[3] : p.p[2];
+      const int pg = (e & 2) ? y : x;
+      const uint8_t* from = kbase + (uint64_t)(uint32_t)(pg < 0 ? 0 : pg) * page_bytes + at * DIM;
+      kc[i] = *reinterpret_cast<const u32x4*>(
+          from + (uint32_t)(((c / KS) & (block - 1)) * DIM + 16 * (c % KS)));
     }
   };
-  auto load_codes = [&](int key0) {
+  auto load_v = [&](const Pages& p, int t) {
+    const int at = (begin + 64 * t) & (block - 1);
+    const int pg = group_of(p);
+    const int64_t first = (int64_t)(uint64_t)(uint32_t)(pg < 0 ? 0 : pg) * page_bytes;
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int c = tid + i * T;
-      const int key = c / KS, ks = c % KS, dim = c >> 2, kst = c & 3;
-      const int hk = pk[i] < 0 ? 0 : pk[i], hv = pv[i] < 0 ? 0 : pv[i];
-      kc[i] = *reinterpret_cast<const u32x4*>(kbase + hk * page_bytes +
-                                              (((key0 + key) & (block - 1)) * DIM + 16 * ks));
-      vc[i] = *reinterpret_cast<const u32x4*>(vbase + hv * page_bytes +
-                                              (dim * block + ((key0 + 16 * kst) & (block - 1))));
-      const int n = stop - (key0 + 16 * kst);
-      live[i] = pv[i] < 0 || n <= 0 ? 0 : (n < 16 ? n : 16);
-      if (ks == 0 && (key & 15) == 0) ksc[i] = a.cache.k_scale[(int64_t)hk * a.cache.heads + kvh];
-      if (i == 0 && dim == 0) vsc = a.cache.v_scale[(int64_t)hv * a.cache.heads + kvh];
+      vc[i] = *reinterpret_cast<const u32x4*>(
+          vbase + first + (uint32_t)((c >> 2) * block + at + ((16 * (c & 3)) & (block - 1))));
+    }
+    if (tid < 4) {
+      const int64_t hp = (int64_t)(pg < 0 ? 0 : pg) * a.cache.heads + kvh;
+      ksc = a.cache.k_scale[hp];
+      vsc = a.cache.v_scale[hp];
     }
   };
-  auto store_tile = [&](int buf) {
+  auto live_of = [&](int pg, int t) {  // keys held of group tid % 4
+    const int n = stop - (begin + 64 * t + 16 * (tid & 3));
+    return pg < 0 || n <= 0 ? 0 : (n < 16 ? n : 16);
+  };
+  auto store_k = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int c = tid + i * T;
-      const int key = c / KS, ks = c % KS, dim = c >> 2, kst = c & 3;
-      f16x8 lo = codes_to_f16<E4M3>(kc[i][0], kc[i][1]);
-      f16x8 hi = codes_to_f16<E4M3>(kc[i][2], kc[i][3]);
+      const int key = c / KS, ks = c % KS;
       // row of the S^T product that gives this key: see above
       const int e = key & 15, m = (key & 16) | ((e & 8) >> 1) | ((e & 4) << 1) | (e & 3);
-      const int swk = KS == 4 ? 2 * ks : ks & 7;
-      lds_k[buf][key >> 5][ks][m ^ swk] = __builtin_bit_cast(u32x4, lo);
-      lds_k[buf][key >> 5][ks][(32 + m) ^ swk] = __builtin_bit_cast(u32x4, hi);
-      if (live[i] < 16) {  // bytes beyond the sequence must not become NaN
+      const int sw = KS == 4 ? 2 * ks : ks & 7;
+      lds_k[buf][key >> 5][ks][m ^ sw] =
+          __builtin_bit_cast(u32x4, codes_to_f16<E4M3>(kc[i][0], kc[i][1]));
+      lds_k[buf][key >> 5][ks][(32 + m) ^ sw] =
+          __builtin_bit_cast(u32x4, codes_to_f16<E4M3>(kc[i][2], kc[i][3]));
+    }
+  };
+  auto store_v = [&](int buf, int live) {
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+      const int c = tid + i * T;
+      const int dim = c >> 2, kst = c & 3;
+      lds_v[buf][kst][dim >> 5][(dim & 31) ^ (2 * kst)] =
+          __builtin_bit_cast(u32x4, codes_to_f16<E4M3>(vc[i][0], vc[i][1]));
+      lds_v[buf][kst][dim >> 5][(32 + (dim & 31)) ^ (2 * kst)] =
+          __builtin_bit_cast(u32x4, codes_to_f16<E4M3>(vc[i][2], vc[i][3]));
+    }
+    if (tid < 4) {
+      const float vs = live > 0 ? vsc : 0.f;
+      lds_ks[buf][tid] = ksc;
+      lds_vs[buf][tid] = vs;
+      lds_lv[buf][tid] = __builtin_amdgcn_logf(vs);
+      lds_iv[buf][tid] = 1.f / vs;
+      lds_live[buf][tid] = live;
+    }
+  };
+  // bytes of v beyond the sequence must not become NaN
+  auto cut_v = [&](int live) {
+    if (__any(live < 16)) {
+#pragma unroll
+      for (int i = 0; i < KC; ++i)
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const int keep = live[i] - 4 * w;
+          const int keep = live - 4 * w;
           vc[i][w] &= keep >= 4 ? 0xffffffffu : (keep <= 0 ? 0u : (1u << (8 * keep)) - 1);
         }
-      }
-      lo = codes_to_f16<E4M3>(vc[i][0], vc[i][1]);
-      hi = codes_to_f16<E4M3>(vc[i][2], vc[i][3]);
-      const int swv = 2 * kst;
-      lds_v[buf][kst][dim >> 5][(dim & 31) ^ swv] = __builtin_bit_cast(u32x4, lo);
-      lds_v[buf][kst][dim >> 5][(32 + (dim & 31)) ^ swv] = __builtin_bit_cast(u32x4, hi);
-      if (ks == 0 && (key & 15) == 0) lds_ks[buf][key >> 4] = ksc[i];
-      if (i == 0 && dim == 0) {
-        lds_vs[buf][kst] = live[0] > 0 ? vsc : 0.f;
-        lds_live[buf][kst] = live[0];
-      }
+    }
+  };
+  auto scores = [&](int buf, f32x16& s0, f32x16& s1) {
+    s0 = f32x16{};
+    s1 = f32x16{};
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const int at = lane ^ (KS == 4 ? 2 * k : k & 7);
+      s0 = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, lds_k[buf][0][k][at]),
+                                                  q[k], s0, 0, 0, 0);
+      s1 = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, lds_k[buf][1][k][at]),
+                                                  q[k], s1, 0, 0, 0);
     }
   };
 
-  if (begin < stop) {
-    load_pages(begin);
-    load_codes(begin);
-    load_pages(begin + 64);
-    store_tile(0);
-    load_codes(begin + 64);
-    load_pages(begin + 128);
-  }
-  int buf = 0;
-  for (int key0 = begin; key0 < stop; key0 += 64, buf ^= 1) {
+  // State at the head of tile t: k(t + 1), v(t) and v's facts in LDS, the
+  // scores of t in registers, the codes of k(t + 2) and v(t + 1) on their way,
+  // pages known to t + 2 and the entries of t + 3 on their way.
+  Pages ahead;
+  int entry, live_next;
+  f32x16 sc0 = {}, sc1 = {};
+  if (n_tiles > 0) {
+    const int e0 = entries(0), e1 = entries(1), e2 = entries(2);
+    entry = entries(3);
+    Pages p0 = pages_of(e0), p1 = pages_of(e1);
+    ahead = pages_of(e2);
+    load_k(p0, 0);
+    load_v(p0, 0);
+    const int live0 = live_of(group_of(p0), 0);
+    cut_v(live0);
+    store_k(0);
+    store_v(0, live0);
+    load_k(p1, 1);
+    load_v(p1, 1);
+    live_next = live_of(group_of(p1), 1);
+    store_k(1);
+    load_k(ahead, 2);
     __syncthreads();
-    if (key0 + 64 < stop) {
-      store_tile(buf ^ 1);
-      load_codes(key0 + 128);
-      load_pages(key0 + 192);
-    }
-    if (!wreal || key0 >= wl.hi || key0 + 64 <= wf.lo) continue;
+    scores(0, sc0, sc1);
+  }
 
-    // ---- S^T
-    f32x16 sc[2];
-    sc[0] = f32x16{};
-    sc[1] = f32x16{};
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const int sw = KS == 4 ? 2 * k : k & 7;
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
-        sc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            __builtin_bit_cast(f16x8, lds_k[buf][kt][k][lane ^ sw]), q[k], sc[kt], 0, 0, 0);
+  auto stage = [&](int t, int live) {  // k(t + 2), v(t + 1); loads of k(t + 3), v(t + 2)
+    store_k(t & 1);
+    store_v((t & 1) ^ 1, live);
+    const Pages p = pages_of(entry);
+    load_k(p, t + 3);
+    load_v(ahead, t + 2);
+    live_next = live_of(group_of(ahead), t + 2);
+    ahead = p;
+    entry = entries(t + 4);
+  };
+  if (!wreal) {  // a wave without rows only stages
+    for (int t = 0; t < n_tiles; ++t) {
+      __syncthreads();
+      cut_v(live_next);
+      stage(t, live_next);
     }
-    float f[4], w[4];
-    float vtop = 0.f;
-    bool full = true;
+    return;
+  }
+  for (int t = 0; t < n_tiles; ++t) {
+    const int buf = t & 1, key0 = begin + 64 * t;
+    __syncthreads();
+    cut_v(live_next);
+#define SC(j) ((j) < 16 ? sc0[(j) & 15] : sc1[(j) & 15])
+    float f[4], lv[4], iv[4];
+    bool full = true, zero = false;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       // (not 0, so that it keeps a masked key's -infinity: a page of zeros)
       f[e] = fmaxf(lds_ks[buf][e] * qf, 0x1p-120f);
-      w[e] = lds_vs[buf][e];
-      vtop = fmaxf(vtop, w[e]);
+      lv[e] = lds_lv[buf][e];
+      iv[e] = lds_iv[buf][e];
       full = full && lds_live[buf][e] == 16;
+      zero = zero || !(lv[e] > -200.f);
     }
-    if (vtop > vref) {  // the same in all lanes
-      const float g = vref / vtop;
+    if (zero) {  // the same in all lanes
 #pragma unroll
-      for (int d = 0; d < DT; ++d) acc[d] = acc[d] * g;
-      vref = vtop;
+      for (int e = 0; e < 4; ++e) {
+        const float vs = lds_vs[buf][e];
+        if (vs > 0.f) {
+          vlast = vs;
+        } else {
+          lv[e] = __builtin_amdgcn_logf(vlast);
+          iv[e] = 1.f / vlast;
+        }
+      }
+    } else {
+      vlast = lds_vs[buf][3];
     }
-    const float vinv = vref > 0.f ? 1.f / vref : 0.f;
-    // (a page of zeros, or one 2^-60 below another, adds nothing to the
-    // output: its w only has to cancel in the sum)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = fmaxf(w[e] * vinv, 0x1p-60f);
-
     if (CAP) {
-      const float ci = 1.f / a.softcap;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < 4; ++e) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float z = sc[e >> 1][8 * (e & 1) + i] * (f[e] * ci);
-          sc[e >> 1][8 * (e & 1) + i] = capped(z) * (a.softcap * kLog2e);
+          const float x = capped(SC(8 * e + i) * f[e]) * (a.softcap * kLog2e);
+          if (e < 2) sc0[8 * e + i] = x; else sc1[8 * (e & 1) + i] = x;
         }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = 1.f;
+        f[e] = 1.f;
+      }
     }
     if (!full || key0 < wl.lo || key0 + 64 > wf.hi) {
 #pragma unroll
@@ -722,7 +813,7 @@ attend_many_kernel(AttendArgs a) {
         for (int i = 0; i < 8; ++i) {
           const int j = key0 + 16 * e + 8 * h + i;
           if (8 * h + i >= live || j < see.lo || j >= see.hi)
-            sc[e >> 1][8 * (e & 1) + i] = -INFINITY;
+            if (e < 2) sc0[8 * e + i] = -INFINITY; else sc1[8 * (e & 1) + i] = -INFINITY;
         }
       }
     }
@@ -730,10 +821,10 @@ attend_many_kernel(AttendArgs a) {
     float top = -INFINITY;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float m = sc[e >> 1][8 * (e & 1)];
+      float m = SC(8 * e);
 #pragma unroll
-      for (int i = 1; i < 8; ++i) m = fmaxf(m, sc[e >> 1][8 * (e & 1) + i]);
-      top = fmaxf(top, m * f[e]);
+      for (int i = 1; i < 8; ++i) m = fmaxf(m, SC(8 * e + i));
+      top = fmaxf(top, fmaf(m, f[e], lv[e]));
     }
     if (__any(top > ref + kSlack)) {
       top = fmaxf(top, __shfl_xor(top, 32));
@@ -744,25 +835,31 @@ attend_many_kernel(AttendArgs a) {
 #pragma unroll
       for (int d = 0; d < DT; ++d) acc[d] = acc[d] * g;
     }
-    // ---- probabilities
+    // ---- probabilities, and the next tile's scores (of the last tile's
+    // successor too: they are not used)
+    f32x16 nx0, nx1;
+    scores(buf ^ 1, nx0, nx1);
     f16x8 p[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float c = __builtin_amdgcn_logf(w[e]) - ref;
+      const float c = lv[e] - ref;
       float part = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
-        const float x = __builtin_amdgcn_exp2f(fmaf(sc[e >> 1][8 * (e & 1) + i], f[e], c));
-        const float y = __builtin_amdgcn_exp2f(fmaf(sc[e >> 1][8 * (e & 1) + i + 1], f[e], c));
+        const float x = __builtin_amdgcn_exp2f(fmaf(SC(8 * e + i), f[e], c));
+        const float y = __builtin_amdgcn_exp2f(fmaf(SC(8 * e + i + 1), f[e], c));
         part += x + y;
         typedef float f32x2 __attribute__((ext_vector_type(2)));
         const f16x2 xy = __builtin_convertvector(f32x2{x, y}, f16x2);
         p[e][i] = xy[0];
         p[e][i + 1] = xy[1];
       }
-      sum = fmaf(part, 1.f / w[e], sum);
+      sum = fmaf(part, iv[e], sum);
     }
-    // ---- O^T += V^T P^T
+    sc0 = nx0;
+    sc1 = nx1;
+    // ---- O^T += V^T P^T, and the next codes
+    stage(t, live_next);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -770,12 +867,13 @@ attend_many_kernel(AttendArgs a) {
         acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
             __builtin_bit_cast(f16x8, lds_v[buf][e][d][lane ^ (2 * e)]), p[e], acc[d], 0, 0, 0);
   }
+#undef SC
 
   sum += __shfl_xor(sum, 32);
   if (!real) return;
   const int64_t out_row = (int64_t)(sp.row0 + tok) * a.q_heads + head;
   if (span.pieces <= 1) {
-    const float inv = sum == 0.f ? 0.f : vref / sum;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint16_t* o = a.out + out_row * DIM + 4 * h;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -796,7 +894,7 @@ attend_many_kernel(AttendArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<f32x4*>(o + 32 * d + 8 * i) =
-            f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]} * vref;
+            f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
     if (h == 0) {
       a.part_ml[2 * at] = ref;
       a.part_ml[2 * at + 1] = sum;
