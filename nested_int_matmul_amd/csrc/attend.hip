@@ -611,9 +611,8 @@ __global__ void __launch_bounds__(NW * 64)
   // this tile's table entries, group lane % 4
   auto entries = [&](int t) {
     const int key = begin + 64 * t + 16 * (lane & 3);
-    int p = -1;
-    if (key < stop) p = table[key >> shift];
-    return p;
+    const int p = table[(key < stop ? key : stop - 1) >> shift];
+    return key < stop ? p : -1;
   };
   auto pages_of = [&](int v) {
     Pages r;
@@ -633,8 +632,7 @@ __global__ void __launch_bounds__(NW * 64)
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int c = tid + i * T;
-      // group of key c / KS: DIM 256: i; 128: wave / 2; 64: wave
-      const int e = DIM == 256 ? i : DIM == 128 ? wave >> 1 : wave;
+      const int e = (wave * (64 / KS) + i * (T / KS)) >> 4;  // group of key c / KS
       const int x = (e & 1) ? p.p[1] : p.p[0], y = (e & 1) ? p.p[3] : p.p[2];
       const int pg = (e & 2) ? y : x;
       const uint8_t* from = kbase + (uint64_t)(uint32_t)(pg < 0 ? 0 : pg) * page_bytes + at * DIM;
@@ -652,11 +650,9 @@ __global__ void __launch_bounds__(NW * 64)
       vc[i] = *reinterpret_cast<const u32x4*>(
           vbase + first + (uint32_t)((c >> 2) * block + at + ((16 * (c & 3)) & (block - 1))));
     }
-    if (tid < 4) {
-      const int64_t hp = (int64_t)(pg < 0 ? 0 : pg) * a.cache.heads + kvh;
-      ksc = a.cache.k_scale[hp];
-      vsc = a.cache.v_scale[hp];
-    }
+    const int64_t hp = (int64_t)(pg < 0 ? 0 : pg) * a.cache.heads + kvh;
+    ksc = a.cache.k_scale[hp];
+    vsc = a.cache.v_scale[hp];
   };
   auto live_of = [&](int pg, int t) {  // keys held of group tid % 4
     const int n = stop - (begin + 64 * t + 16 * (tid & 3));
@@ -676,7 +672,7 @@ __global__ void __launch_bounds__(NW * 64)
           __builtin_bit_cast(u32x4, codes_to_f16<E4M3>(kc[i][2], kc[i][3]));
     }
   };
-  auto store_v = [&](int buf, int live) {
+  auto store_v = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int c = tid + i * T;
@@ -686,6 +682,9 @@ __global__ void __launch_bounds__(NW * 64)
       lds_v[buf][kst][dim >> 5][(32 + (dim & 31)) ^ (2 * kst)] =
           __builtin_bit_cast(u32x4, codes_to_f16<E4M3>(vc[i][2], vc[i][3]));
     }
+  };
+  // the tile's scales and keys held
+  auto store_facts = [&](int buf, int live) {
     if (tid < 4) {
       const float vs = live > 0 ? vsc : 0.f;
       lds_ks[buf][tid] = ksc;
@@ -736,7 +735,8 @@ __global__ void __launch_bounds__(NW * 64)
     const int live0 = live_of(group_of(p0), 0);
     cut_v(live0);
     store_k(0);
-    store_v(0, live0);
+    store_v(0);
+    store_facts(0, live0);
     load_k(p1, 1);
     load_v(p1, 1);
     live_next = live_of(group_of(p1), 1);
@@ -746,9 +746,9 @@ __global__ void __launch_bounds__(NW * 64)
     scores(0, sc0, sc1);
   }
 
-  auto stage = [&](int t, int live) {  // k(t + 2), v(t + 1); loads of k(t + 3), v(t + 2)
+  auto stage = [&](int t) {  // k(t + 2), v(t + 1); loads of k(t + 3), v(t + 2)
     store_k(t & 1);
-    store_v((t & 1) ^ 1, live);
+    store_v((t & 1) ^ 1);
     const Pages p = pages_of(entry);
     load_k(p, t + 3);
     load_v(ahead, t + 2);
@@ -760,7 +760,8 @@ __global__ void __launch_bounds__(NW * 64)
     for (int t = 0; t < n_tiles; ++t) {
       __syncthreads();
       cut_v(live_next);
-      stage(t, live_next);
+      store_facts((t & 1) ^ 1, live_next);
+      stage(t);
     }
     return;
   }
@@ -768,6 +769,7 @@ __global__ void __launch_bounds__(NW * 64)
     const int buf = t & 1, key0 = begin + 64 * t;
     __syncthreads();
     cut_v(live_next);
+    store_facts(buf ^ 1, live_next);
 #define SC(j) ((j) < 16 ? sc0[(j) & 15] : sc1[(j) & 15])
     float f[4], lv[4], iv[4];
     bool full = true, zero = false;
@@ -859,7 +861,7 @@ __global__ void __launch_bounds__(NW * 64)
     sc0 = nx0;
     sc1 = nx1;
     // ---- O^T += V^T P^T, and the next codes
-    stage(t, live_next);
+    stage(t);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
