@@ -463,8 +463,8 @@ __global__ void __launch_bounds__(NW * 64)
       if (direct) {
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         u32x2 b;
-        b[0] = bf16_rne(o[0] * inv) | (bf16_rne(o[1] * inv) << 16);
-        b[1] = bf16_rne(o[2] * inv) | (bf16_rne(o[3] * inv) << 16);
+        b[0] = bf16_pair(o[0] * inv, o[1] * inv);
+        b[1] = bf16_pair(o[2] * inv, o[3] * inv);
         if (ll == 0.f) b = u32x2{0, 0};
         *reinterpret_cast<u32x2*>(a.out + out_row * DIM + d) = b;
         if (a.lse && d == 0) a.lse[out_row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
@@ -882,8 +882,8 @@ __global__ void __launch_bounds__(NW * 64)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         u32x2 b;
-        b[0] = bf16_rne(acc[d][4 * i] * inv) | (bf16_rne(acc[d][4 * i + 1] * inv) << 16);
-        b[1] = bf16_rne(acc[d][4 * i + 2] * inv) | (bf16_rne(acc[d][4 * i + 3] * inv) << 16);
+        b[0] = bf16_pair(acc[d][4 * i] * inv, acc[d][4 * i + 1] * inv);
+        b[1] = bf16_pair(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv);
         if (sum == 0.f) b = u32x2{0, 0};
         *reinterpret_cast<u32x2*>(o + 32 * d + 8 * i) = b;
       }
@@ -973,8 +973,8 @@ __global__ void __launch_bounds__(256) join_kernel(AttendArgs a, int tile_rows) 
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   u32x2 b;
-  b[0] = bf16_rne(o[0] * inv) | (bf16_rne(o[1] * inv) << 16);
-  b[1] = bf16_rne(o[2] * inv) | (bf16_rne(o[3] * inv) << 16);
+  b[0] = bf16_pair(o[0] * inv, o[1] * inv);
+  b[1] = bf16_pair(o[2] * inv, o[3] * inv);
   if (sum == 0.f) b = u32x2{0, 0};
   *reinterpret_cast<u32x2*>(a.out + out_row * DIM + 4 * l) = b;
   if (a.lse && l == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;

@@ -79,7 +79,8 @@ hipError_t launch_rope(const RopeSpec& r, const int* positions, const void* x, b
 // (four of fp32) are in flight before the first is used, the first of them
 // before the page is known.  k's angles of a thread advance by a constant
 // step, so its sines and cosines follow by one complex product a token in
-// place of an evaluation.
+// place of an evaluation, and its first ones from a table of the page's first
+// position and of one position (turn_table).
 // Rounding: a product with 1 / scale decides unless the quotient is within its
 // error of a border between codes; only then is the exact quotient's side
 // found (exact_quotient).
@@ -96,15 +97,34 @@ constexpr int kQueryTokens = 8;
 template <int DIM, int T, bool F32>
 __device__ __forceinline__ void append_queries(const RopeSpec& r, const SeqSpan& sp, int64_t lo,
                                                int64_t hi, const void* q, int64_t q_stride,
-                                               int q_heads, uint16_t* q_out) {
+                                               int q_heads, uint16_t* q_out, double* table) {
   constexpr int U = DIM / 8, SLOTS = T / U;
   const int u = threadIdx.x % U, slot = threadIdx.x / U;
   const int hs = q_heads < SLOTS ? q_heads : SLOTS;  // heads side by side
   const int toks = SLOTS / hs;                       // tokens side by side
   const int head0 = slot % hs, tok0 = slot / hs;
-  if (tok0 >= toks) return;
   const Unit un = unit_of(u, r.freq ? r.rot : 0, r.interleaved);
   Turn turn, step;
+  if (r.freq) {
+    turn_table(table, r, (double)lo);
+    if (un.turns) {
+      // turn at lo + tok0, step of toks positions
+      turn.from_table(table, un);
+      if (hi - lo > 1) {
+        Turn power;
+        power.from_table(table + r.rot, un);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) step.c[i] = 1.0, step.s[i] = 0.0;
+        for (int b = 1; b <= toks; b <<= 1) {
+          if (tok0 & b) turn.advance(power);
+          if (toks & b) step.advance(power);
+          const Turn p = power;
+          power.advance(p);
+        }
+      }
+    }
+  }
+  if (tok0 >= toks) return;
   for (int64_t pos = lo + tok0; pos < hi; pos += toks) {
     const int64_t row = sp.row0 + (pos - sp.start);
     for (int h = head0; h < q_heads; h += 4 * hs) {
@@ -113,14 +133,7 @@ __device__ __forceinline__ void append_queries(const RopeSpec& r, const SeqSpan&
       for (int j = 0; j < 4; ++j)
         if (h + j * hs < q_heads)
           raw[j] = load_unit<F32>(q, row * q_stride + (int64_t)(h + j * hs) * DIM, un);
-      if (h == head0 && un.turns) {
-        if (pos == lo + tok0) {
-          turn.at(r, un, (double)pos, r.factor);
-          if (pos + toks < hi) step.at(r, un, (double)toks, 1.0);
-        } else {
-          turn.advance(step);
-        }
-      }
+      if (h == head0 && un.turns && pos != lo + tok0) turn.advance(step);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (h + j * hs >= q_heads) continue;
@@ -169,7 +182,10 @@ append_kernel(KvCache cache, KvBatch b, RopeSpec r, const void* k, const void* v
   constexpr int ONCE = F32 ? 4 : 8;            // steps loaded before the first is used
   constexpr int G = STEPS < 4 ? STEPS : 4;     // consecutive tokens a thread has of v
   constexpr int PITCH = BLOCK + 4;             // bytes of a dim's row in LDS
-  __shared__ uint32_t tile[DIM * PITCH / 4];
+  // v's codes on their way to dim-major, or k's and q's table of turns
+  __shared__ __align__(16) uint32_t tile[DIM * PITCH / 4];
+  static_assert(sizeof(tile) >= 16 * DIM, "turns of DIM / 2 pairs, twice");
+  double* const table = reinterpret_cast<double*>(tile);
   __shared__ uint32_t wave_max[T / 64];
 
   const int seq = blockIdx.z;
@@ -187,7 +203,8 @@ append_kernel(KvCache cache, KvBatch b, RopeSpec r, const void* k, const void* v
     lo = lo > base + part * kQueryTokens ? lo : base + part * kQueryTokens;
     const int64_t last = base + (part + 1) * kQueryTokens;
     hi = hi < last ? hi : last;
-    if (lo < hi) append_queries<DIM, T, F32>(r, sp, lo, hi, q, q_stride, q_heads, q_out);
+    if (lo < hi) 
+      append_queries<DIM, T, F32>(r, sp, lo, hi, q, q_stride, q_heads, q_out, table);
     return;
   }
   const int page = page_of(b, seq, pi, cache.pages);
@@ -218,9 +235,20 @@ append_kernel(KvCache cache, KvBatch b, RopeSpec r, const void* k, const void* v
       const int t = place(j);
       if (t >= used && t < fill) raw[j - j0] = load_unit<F32>(src, at0 + t * kv_stride, un);
     }
-    if (j0 == 0 && un.turns) {
-      turn.at(r, un, (double)(base + slot), r.factor);
-      if (STEPS > 1) step.at(r, un, (double)SLOTS, 1.0);
+    if (j0 == 0 && !is_v && r.freq) {
+      turn_table(table, r, (double)base);
+      if (un.turns) {
+        // turn at base + slot; the step of SLOTS positions is what is left of
+        // one position's after its squarings
+        turn.from_table(table, un);
+        step.from_table(table + r.rot, un);
+#pragma unroll
+        for (int b = 1; b < SLOTS; b <<= 1) {
+          turn.advance_if(slot & b, step);
+          const Turn p = step;
+          step.advance(p);
+        }
+      }
     }
 #pragma unroll
     for (int j = j0; j < j0 + ONCE && j < STEPS; ++j) {

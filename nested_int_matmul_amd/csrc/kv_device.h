@@ -258,15 +258,22 @@ __device__ __forceinline__ void numbers_of_unit(const RawUnit<F32>& r, float* v)
 
 // Turn the unit's four pairs by (c, s) in float64, each result rounded once
 // to fp32.
-__device__ __forceinline__ void turn_unit(float* v, const double* c, const double* s,
-                                          bool interleaved) {
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn_pairs(float* v, const double* c, const double* s) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int i1 = interleaved ? 2 * i : i, i2 = interleaved ? 2 * i + 1 : 4 + i;
-    const double x1 = v[i1], x2 = v[i2];
-    v[i1] = (float)(x1 * c[i] - x2 * s[i]);
-    v[i2] = (float)(x2 * c[i] + x1 * s[i]);
+    constexpr int A = INTERLEAVED ? 2 : 1, B = INTERLEAVED ? 1 : 4;
+    const double x1 = v[A * i], x2 = v[A * i + B];
+    v[A * i] = (float)(x1 * c[i] - x2 * s[i]);
+    v[A * i + B] = (float)(x2 * c[i] + x1 * s[i]);
   }
+}
+__device__ __forceinline__ void turn_unit(float* v, const double* c, const double* s,
+                                          bool interleaved) {
+  if (interleaved)
+    turn_pairs<true>(v, c, s);
+  else
+    turn_pairs<false>(v, c, s);
 }
 
 // Sines and cosines of a unit's four pairs at one position, times the factor;
@@ -282,6 +289,7 @@ struct Turn {
       c[i] *= factor;
     }
   }
+  // one after the other
   __device__ __forceinline__ void advance(const Turn& d) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -290,18 +298,50 @@ struct Turn {
       c[i] = n;
     }
   }
+  __device__ __forceinline__ void advance_if(bool yes, const Turn& d) {
+    Turn t = *this;
+    t.advance(d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = yes ? t.c[i] : c[i];
+      s[i] = yes ? t.s[i] : s[i];
+    }
+  }
+  __device__ __forceinline__ void from_table(const double* table, const Unit& u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = table[2 * (u.pair0 + i)];
+      s[i] = table[2 * (u.pair0 + i) + 1];
+    }
+  }
 };
 
-// fp32 -> bf16 bits, nearest even; NaN stays a NaN.
-__device__ __forceinline__ uint32_t bf16_rne(float f) {
-  const uint32_t u = __float_as_uint(f);
-  const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-  return (u & 0x7fffffffu) > 0x7f800000u ? ((u >> 16) | 0x40u) : r;
+// A workgroup's table (in LDS) of the turns of all pairs at position `pos`
+// (times the factor), then of one position: one evaluation a thread for both,
+// where every thread by itself would make eight.  Ends with a barrier.
+__device__ __forceinline__ void turn_table(double* table, const RopeSpec& r, double pos) {
+  const int pairs = r.rot >> 1;
+  for (int i = threadIdx.x; i < 2 * pairs; i += blockDim.x) {
+    const bool one = i >= pairs;
+    double sn, cs;
+    sincos64((one ? 1.0 : pos) * r.freq[one ? i - pairs : i], &sn, &cs);
+    const double f = one ? 1.0 : r.factor;
+    table[2 * i] = cs * f;
+    table[2 * i + 1] = sn * f;
+  }
+  __syncthreads();
+}
+
+// A pair of fp32 -> bf16 bits, nearest even; NaN stays a NaN.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 // Four dwords of bf16 pairs: the unit's lo run in w[0..1], its hi run in w[2..3].
 __device__ __forceinline__ void pack_unit(const float* v, uint32_t* w) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = bf16_rne(v[2 * i]) | (bf16_rne(v[2 * i + 1]) << 16);
+  for (int i = 0; i < 4; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
 }
 
 }  // namespace mq
