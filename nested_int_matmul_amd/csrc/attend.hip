@@ -125,7 +125,7 @@ __device__ __forceinline__ int held_of(const AttendArgs& a, int s) {
 // Waves of a SIMD that the registers are cut for (k and v of a tile, the
 // outputs, the queries).
 constexpr int few_waves(int dim, int rows, int kt) {
-  return dim * (rows + kt / 32) <= 256 ? 3 : dim * (rows + kt / 32) <= 512 ? 2 : 1;
+  return  dim * (rows + kt / 32) <= 256 ? 3 : dim * (rows + kt / 32) <= 512 ? 2 : 1;
 }
 
 template <int DIM, int ROWS, int KT, int NW, bool E4M3, bool CAP>
@@ -997,9 +997,8 @@ constexpr int kFewWaves = 4;
 // against 107 us).
 constexpr int few_keys(int dim) { return dim == 128 ? 64 : 32; }
 
-template <int DIM, int ROWS, int NW>
+template <int DIM, int ROWS, int NW, int KT>
 hipError_t few(const AttendArgs& a, dim3 grid, hipStream_t s) {
-  constexpr int KT = few_keys(DIM);
   const dim3 block(NW * 64);
   const bool cap = a.softcap > 0.f;
   if (a.cache.e4m3) {
@@ -1041,8 +1040,9 @@ hipError_t attend_dim(AttendArgs& a, hipStream_t s) {
   const int tile = rows_tile(most, a.cache.dim);
   const dim3 grid((unsigned)(a.cache.heads * ((most + tile - 1) / tile)), (unsigned)a.pieces,
                   (unsigned)a.batch.seqs);
-  hipError_t e = tile == 16   ? few<DIM, 1, kFewWaves>(a, grid, s)
-                 : tile == 32 ? few<DIM, 2, kFewWaves>(a, grid, s)
+  constexpr int KT = few_keys(DIM);
+  hipError_t e = tile == 16   ? few<DIM, 1, kFewWaves, KT>(a, grid, s)
+                 : tile == 32 ? few<DIM, 2, kFewWaves, KT>(a, grid, s)
                               : many<DIM>(a, grid, s);
   if (e != hipSuccess || a.pieces <= 1) return e;
   const dim3 jg((unsigned)most, (unsigned)a.cache.heads, (unsigned)a.batch.seqs);
@@ -1062,12 +1062,13 @@ size_t attend_plan(AttendArgs& a) {
   // Two workgroups a CU; with several sequences, whose lengths the host does
   // not know, at least 16 pieces of the longest possible one, so that long
   // sequences do not run on behind short ones; and 512 tokens a piece where
-  // that still fills the chip, 256 (one tile a wave) where it does not.
+  // that still fills the chip, 256 where it does not.
   int64_t pieces = (512 + groups - 1) / groups;
   if (tile <= 32 && a.batch.seqs > 1 && pieces < 16) pieces = 16;
-  int64_t piece = (keys + pieces - 1) / pieces;
-  const int64_t least = groups * keys >= 512 * 256 ? 512 : 64 * kFewWaves;
-  piece = (piece + least - 1) / least * least;
+  const int64_t least = groups * keys >= 512 * 256 ? 512 : 256;
+  if (pieces > (keys + least - 1) / least) pieces = (keys + least - 1) / least;
+  const int64_t grain = tile <= 32 ? few_keys(a.cache.dim) * kFewWaves : 64;
+  const int64_t piece = ((keys + pieces - 1) / pieces + grain - 1) / grain * grain;
   a.piece = (int)piece;
   a.pieces = (int)((keys + piece - 1) / piece);
   if (a.pieces <= 1) {

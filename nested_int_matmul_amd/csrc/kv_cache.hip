@@ -81,9 +81,6 @@ hipError_t launch_rope(const RopeSpec& r, const int* positions, const void* x, b
 // step, so its sines and cosines follow by one complex product a token in
 // place of an evaluation, and its first ones from a table of the page's first
 // position and of one position (turn_table).
-// Rounding: a product with 1 / scale decides unless the quotient is within its
-// error of a border between codes; only then is the exact quotient's side
-// found (exact_quotient).
 // v is held dim-major: pages that get 16 tokens or more go through LDS, four
 // tokens of a dim to a dword, and leave in 16-byte pieces; fewer tokens go out
 // as single bytes.
@@ -150,25 +147,6 @@ __device__ __forceinline__ void append_queries(const RopeSpec& r, const SeqSpan&
   }
 }
 
-// Codes of a unit (four dwords of bf16 pairs) from exact quotients.
-__device__ __forceinline__ void exact_codes(const uint32_t* w, float s, float rs, bool e4m3,
-                                            uint32_t* out) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t pair = w[2 * h + (i >> 1)];
-      const uint32_t bits = (i & 1) ? pair >> 16 : pair & 0xffffu;
-      const uint32_t mag = bits & 0x7fffu;
-      y[i] = exact_quotient(__uint_as_float(bits << 16), s, rs);
-      if (mag >= 0x7f80u)  // infinity: beyond every code, NaN: 0
-        y[i] = mag > 0x7f80u ? 0.f : ((bits & 0x8000u) ? -1e9f : 1e9f);
-    }
-    out[h] = codes_of(y, e4m3);
-  }
-}
-
 // Threads of a page's workgroup: at most 64 values each.
 constexpr int append_threads(int dim, int block) { return dim * block > 16384 ? 512 : 256; }
 
@@ -227,6 +205,9 @@ append_kernel(KvCache cache, KvBatch b, RopeSpec r, const void* k, const void* v
   typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
   u16x2 pair_top = {0, 0};
   Turn turn, step;
+  const bool single = fill - used == 1;
+  int64_t ph = 0;
+  float was = 0.f;
 #pragma unroll
   for (int j0 = 0; j0 < STEPS; j0 += ONCE) {
     RawUnit<F32> raw[ONCE];
@@ -235,9 +216,17 @@ append_kernel(KvCache cache, KvBatch b, RopeSpec r, const void* k, const void* v
       const int t = place(j);
       if (t >= used && t < fill) raw[j - j0] = load_unit<F32>(src, at0 + t * kv_stride, un);
     }
+    if (j0 == 0) {
+      // (of the pool's first page where there is none: not used)
+      ph = (int64_t)(page < 0 ? 0 : page) * cache.heads + head;
+      if (used > 0) was = (is_v ? cache.v_scale : cache.k_scale)[ph];
+    }
     if (j0 == 0 && !is_v && r.freq) {
-      turn_table(table, r, (double)base);
-      if (un.turns) {
+      // (a single token: its own turn)
+      turn_table(table, r, (double)(single ? base + used : base));
+      if (un.turns && single) {
+        turn.from_table(table, un);
+      } else if (un.turns) {
         // turn at base + slot; the step of SLOTS positions is what is left of
         // one position's after its squarings
         turn.from_table(table, un);
@@ -270,14 +259,12 @@ append_kernel(KvCache cache, KvBatch b, RopeSpec r, const void* k, const void* v
           pair_top = __builtin_elementwise_max(
               pair_top, __builtin_bit_cast(u16x2, w[j][i] & 0x7fff7fffu));
       }
-      if (un.turns && j + 1 < STEPS) turn.advance(step);
+      if (un.turns && !single && j + 1 < STEPS) turn.advance(step);
     }
   }
   if (page < 0) return;  // (uniform: the page is the workgroup's)
-  const int64_t ph = (int64_t)page * cache.heads + head;
   float* scale_at = (is_v ? cache.v_scale : cache.k_scale) + ph;
   uint8_t* codes = (is_v ? cache.v : cache.k) + ph * (DIM * BLOCK);
-  const float was = used > 0 ? *scale_at : 0.f;
   uint32_t top = pair_top[0] > pair_top[1] ? pair_top[0] : pair_top[1];
   // the largest of the workgroup; if some value is no number, of the numbers
   bool odd = false;
@@ -313,10 +300,11 @@ append_kernel(KvCache cache, KvBatch b, RopeSpec r, const void* k, const void* v
 
   // ---- earlier codes, where the scale grows
   if (grows) {
+    const double ratio = (double)was / (double)now;
     if (!is_v) {
       for (int i = tid; i < used * (DIM / 4); i += T) {
         uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
-        *p = recode(*p, e4m3, was, now);
+        *p = recode(*p, e4m3, ratio);
       }
     } else {
       // four tokens of a dim at a time; those at or beyond `used` keep their
@@ -325,7 +313,7 @@ append_kernel(KvCache cache, KvBatch b, RopeSpec r, const void* k, const void* v
       for (int i = tid; i < per * DIM; i += T) {
         const int d = i / per, t = (i % per) * 4;
         uint32_t* p = reinterpret_cast<uint32_t*>(codes + d * BLOCK + t);
-        const uint32_t before = *p, after = recode(before, e4m3, was, now);
+        const uint32_t before = *p, after = recode(before, e4m3, ratio);
         const int keep = used - t;
         const uint32_t m = keep >= 4 ? 0xffffffffu : (1u << (8 * keep)) - 1;
         *p = (after & m) | (before & ~m);
@@ -355,8 +343,13 @@ append_kernel(KvCache cache, KvBatch b, RopeSpec r, const void* k, const void* v
           const uint32_t pair = w[j][i >> 1];
           x[i] = __uint_as_float((i & 1) ? pair & 0xffff0000u : pair << 16);
         }
-        const bool near = quick_codes(x, rs, e4m3, out[j - j0]);
-        if (near || odd) exact_codes(w[j], now, rs, e4m3, out[j - j0]);
+        if (odd) {  // infinity: the largest code, NaN: 0
+          const float most = now * (e4m3 ? 448.f : 127.f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -most), most);
+        }
+        codes_of_values(x, now, rs, e4m3, out[j - j0]);
       }
       if (!is_v) {
         *reinterpret_cast<uint32_t*>(codes + t * DIM + un.lo) = out[j - j0][0];

@@ -9,8 +9,8 @@ namespace mq {
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// Smallest scale of a page with codes other than 0.  Above it the remainder
-// of a division by the scale stays a normal fp32 number (see exact_quotient).
+// Smallest scale of a page with codes other than 0: multiples of the scale by
+// half codes, and what is left of a value beside them, are fp32 numbers.
 constexpr float kMinScale = 0x1p-100f;
 
 // 1 / (largest code) as fp32
@@ -42,25 +42,6 @@ __device__ __forceinline__ int page_of(const KvBatch& b, int s, int64_t pi, int 
 }
 
 // ---- rounding to codes
-// x / s rounded to odd at fp32: the quotient cut towards zero, its last bit
-// set if anything was cut.  A later rounding to fewer bits then equals the
-// rounding of the exact quotient.  rs = 1 / s.  One correction step brings
-// the first estimate within an ulp; the remainder's sign (exact in one fma:
-// s >= 2^-100 keeps it normal wherever a code is near a border) says on which
-// side the quotient lies.
-__device__ __forceinline__ float exact_quotient(float x, float s, float rs) {
-  float y = x * rs;
-  y = fmaf(fmaf(-y, s, x), rs, y);
-  const float rem = fmaf(-y, s, x);
-  int bits = __float_as_int(y);
-  // remainder against the quotient's sign: |x / s| < |y|
-  if (rem != 0.f) {
-    if ((__float_as_int(rem) ^ __float_as_int(x)) < 0) bits -= 1;
-    bits |= 1;
-  }
-  return __int_as_float(bits);
-}
-
 // fp64 -> fp32 rounded to odd
 __device__ __forceinline__ float f64_to_f32_odd(double q) {
   const float f = (float)q;
@@ -72,50 +53,54 @@ __device__ __forceinline__ float f64_to_f32_odd(double q) {
   return __int_as_float(bits);
 }
 
-// Quotients x * rs of eight values, good to 2^-23 of themselves, to code bytes,
-// and whether one of them is so near a border between two codes (or on it) that
-// only the exact quotient can tell.  For finite values up to the scale's range.
-__device__ __forceinline__ bool quick_codes(const float* x, float rs, bool e4m3, uint32_t* out) {
+// Eight values x to the codes nearest to the exact quotients x / s, ties to
+// even; rs = 1 / s.  |x| rs, good to 2^-23 of itself, names the interval
+// between two codes, whose one border b (half way) has so few bits that the
+// sign of |x| - b s is exact in one fma (s >= 2^-100: nothing underflows).  The
+// border, moved by that sign in its last bit, then rounds the way the exact
+// quotient does, and to even if the quotient is the border; an estimate next to
+// a code may name the interval on the other side of it, whose border sends it
+// back to the same code.  bf16 values meet borders all the time (one in a
+// hundred where 1 / s has few bits), so this is done for all of them, without
+// branches.
+__device__ __forceinline__ void codes_of_values(const float* x, float s, float rs, bool e4m3,
+                                                uint32_t* out) {
+  auto beside = [&](float b, float ax) {  // b moved towards the quotient
+    const int e = __float_as_int(fmaf(-b, s, ax));
+    return __int_as_float(__float_as_int(b) + (e > 1 ? 1 : e < -1 ? -1 : e));
+  };
   if (e4m3) {
-    // A border has one bit set below the three of a code's mantissa: in the
-    // low 20 bits of the quotient, or of 2^-6 plus it where codes are
-    // subnormal (their spacing is that of [2^-6, 2^-5)).  Four units in the
-    // last place on each side cover the error (two) and that sum's (one).
-    uint32_t near = 0xffffffffu;
+    // three mantissa bits; below 2^-6 the spacing of [2^-6, 2^-5)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float y[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        y[i] = x[4 * h + i] * rs;
-        const float m = fabsf(y[i]);
-        const float z = m < 0x1p-6f ? m + 0x1p-6f : m;
-        const uint32_t t = (__float_as_uint(z) + (4u - 0x80000u)) & 0xfffffu;
-        near = t < near ? t : near;
+        const float v = x[4 * h + i], ax = fabsf(v), m = ax * rs;
+        const float low = m < 0x1p-6f ? 0x1p-6f : 0.f;
+        const uint32_t z = (__float_as_uint(m + low) & 0xfff00000u) | 0x00080000u;
+        y[i] = copysignf(beside(__uint_as_float(z) - low, ax), v);
       }
-      int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+      const int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
       out[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
     }
-    return near <= 8u;
+    return;
   }
-  // 1.5 * 2^23 added rounds to the nearest integer, ties to even, and leaves
-  // it in the low byte; |y| <= 127 is off by less than 2^-16.
-  float worst = 0.f;
+  // 1.5 * 2^23 added rounds to the nearest integer, ties to even, and leaves it
+  // in the low byte
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t z[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float y = x[4 * h + i] * rs;
-      const float r = y + 12582912.f;
-      z[i] = __float_as_uint(r);
-      worst = fmaxf(worst, fabsf(y - (r - 12582912.f)));
+      const float v = x[4 * h + i], ax = fabsf(v);
+      const float b = __builtin_floorf(ax * rs) + 0.5f;
+      z[i] = __float_as_uint(copysignf(beside(b, ax), v) + 12582912.f);
     }
-    const uint32_t a = __builtin_amdgcn_perm(z[1], z[0], 0x0c0c0400u);
-    const uint32_t b = __builtin_amdgcn_perm(z[3], z[2], 0x04000c0cu);
-    out[h] = a | b;
+    const uint32_t lo = __builtin_amdgcn_perm(z[1], z[0], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(z[3], z[2], 0x04000c0cu);
+    out[h] = lo | hi;
   }
-  return worst >= 0.5f - 0x1p-15f;
 }
 
 // Four quotients (rounded to odd) to four code bytes.
@@ -151,14 +136,20 @@ __device__ __forceinline__ void numbers_of(uint32_t w, bool e4m3, float* y) {
   }
 }
 
-// Four code bytes whose page's scale grows from `was` to `now`.
-__device__ __forceinline__ uint32_t recode(uint32_t w, bool e4m3, double was, double now) {
+// Four code bytes whose page's scale grows, by ratio = was / now in float64.
+// A product with it is off by 2^-52 of itself at most; a quotient that is not
+// on a border between codes is at least 2^-34 of itself away from one (both
+// scales have 24 bits, codes and borders 8), so rounding the product to 41
+// bits first puts the quotients that are on one exactly there.
+__device__ __forceinline__ uint32_t recode(uint32_t w, bool e4m3, double ratio) {
   float y[4];
   numbers_of(w, e4m3, y);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float q = f64_to_f32_odd((double)y[i] * was / now);
-    y[i] = q == q ? q : 0.f;
+    const double q = (double)y[i] * ratio;
+    const double wide = q * 4097.0;  // 2^12 + 1
+    const float f = f64_to_f32_odd(wide - (wide - q));
+    y[i] = f == f ? f : 0.f;
   }
   return codes_of(y, e4m3);
 }
