@@ -1061,11 +1061,11 @@ size_t attend_plan(AttendArgs& a) {
   const int64_t groups = (int64_t)a.batch.seqs * a.cache.heads * ((most + tile - 1) / tile);
   // Two workgroups a CU; with several sequences, whose lengths the host does
   // not know, at least 16 pieces of the longest possible one, so that long
-  // sequences do not run on behind short ones; and 512 tokens a piece where
+  // sequences do not run on behind short ones; and 384 tokens a piece where
   // that still fills the chip, 256 where it does not.
   int64_t pieces = (512 + groups - 1) / groups;
   if (tile <= 32 && a.batch.seqs > 1 && pieces < 16) pieces = 16;
-  const int64_t least = groups * keys >= 512 * 256 ? 512 : 256;
+  const int64_t least = groups * keys >= 512 * 256 ? 384 : 256;
   if (pieces > (keys + least - 1) / least) pieces = (keys + least - 1) / least;
   const int64_t grain = tile <= 32 ? few_keys(a.cache.dim) * kFewWaves : 64;
   const int64_t piece = ((keys + pieces - 1) / pieces + grain - 1) / grain * grain;
