@@ -502,10 +502,11 @@ MQ_API mq_status mq_rope(const mq_rope_spec* rope, const int32_t* positions, con
  *   k, v   bf16 or fp32 (x_type) [rows, heads, dim], rows every kv_stride
  *   q      same type [rows, q_heads, dim], rows every q_stride; or NULL
  *   q_out  bf16 bits [rows, q_heads, dim] contiguous; NULL exactly if q is
- * Alignment as mq_rope (strides multiples of 8; 16-byte pointers).  No two
- * sequences of one call may write the same page (a page shared for reading,
- * such as a common prefix, is fine if it is full); if they do, that page's
- * contents are unspecified.  1 <= q_heads, q_heads * dim <= 2^20.
+ * Alignment as mq_rope (strides multiples of 8; 16-byte pointers).  A page may
+ * be written for one place of one sequence only in a call (a page shared for
+ * reading, such as a common prefix, is fine if it is full); if two write it,
+ * its contents are unspecified.  Rows at positions below 0 (kv_len smaller
+ * than n) are skipped, their q_out too.  1 <= q_heads, q_heads * dim <= 2^20.
  */
 MQ_API mq_status mq_cache_append(const mq_kv_cache* cache, const mq_kv_batch* batch,
                           const mq_rope_spec* rope, const void* k, const void* v,
@@ -535,8 +536,8 @@ MQ_API mq_status mq_cache_read(const mq_kv_cache* cache, const mq_kv_batch* batc
  *   q    bf16 bits [rows, q_heads, dim], rows every q_stride entries
  *   out  bf16 bits [rows, q_heads, dim] contiguous
  *   lse  fp32 [rows, q_heads] contiguous, or NULL
- *   causal in {0, 1}; window >= 0 (0: none; only with causal); softcap >= 0,
- *   finite; scale finite
+ *   causal in {0, 1}; window >= 0 (0: none; only with causal); softcap 0
+ *   (none) or in [1e-6, 1e6]; scale finite
  *   workspace  at least mq_cache_attend_workspace_bytes(...) bytes, 256-byte
  *              aligned (may be NULL when that is 0): partial results of long
  *              sequences cut into pieces.  Calls that may overlap in time

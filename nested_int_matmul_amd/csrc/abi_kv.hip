@@ -127,8 +127,8 @@ mq_status attend_check(const mq_kv_cache* cache, const mq_kv_batch* batch, const
   if (!q || !out) return MQ_ERR_NULL;
   mq_status s = check_attend(cache, batch, q_heads, window);
   if (s != MQ_OK) return s;
-  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f ||
-      (softcap > 0.f && softcap < 1e-30f) || (causal != 0 && causal != 1))
+  if (!std::isfinite(scale) || !(softcap >= 0.f && softcap <= 1e6f) ||
+      (softcap > 0.f && softcap < 1e-6f) || (causal != 0 && causal != 1))
     return MQ_ERR_PRECISION;
   if (window > 0 && !causal) return MQ_ERR_SHAPE;
   if ((s = check_strided(q, q_stride, q_heads * cache->dim)) != MQ_OK) return s;
