@@ -543,7 +543,7 @@ MQ_API mq_status mq_cache_read(const mq_kv_cache* cache, const mq_kv_batch* batc
  *              sequences cut into pieces.  Calls that may overlap in time
  *              need workspaces of their own.
  * Sizes: q_heads a multiple of heads, at most 1024 times it; q_heads * dim <=
- * 2^20; max_new * q_heads <= 2^24; rows * q_heads < 2^31; q, out 16-byte aligned,
+ * 2^20; max_new * q_heads <= 2^24; rows * q_heads <= 2^25; q, out 16-byte aligned,
  * q_stride a multiple of 8 and >= q_heads * dim.
  */
 MQ_API size_t mq_cache_attend_workspace_bytes(const mq_kv_cache* cache, const mq_kv_batch* batch,

@@ -77,7 +77,7 @@ mq_status check_attend(const mq_kv_cache* c, const mq_kv_batch* b, int64_t q_hea
       q_heads / c->heads > 1024)
     return MQ_ERR_SHAPE;
   if ((int64_t)b->max_new * q_heads > (int64_t)1 << 24) return MQ_ERR_SHAPE;
-  if (b->rows * q_heads > 0x7fffffff) return MQ_ERR_SHAPE;
+  if (b->rows * q_heads > (int64_t)1 << 25) return MQ_ERR_SHAPE;  // 64 threads each, one grid
   if (window < 0) return MQ_ERR_SHAPE;
   return MQ_OK;
 }
@@ -192,8 +192,7 @@ mq_status mq_cache_read(const mq_kv_cache* cache, const mq_kv_batch* batch, void
 size_t mq_cache_attend_workspace_bytes(const mq_kv_cache* cache, const mq_kv_batch* batch,
                                        int64_t q_heads, int64_t window) {
   if (check_attend(cache, batch, q_heads, window) != MQ_OK) return 0;
-  mq::AttendArgs a = attend_args(cache, batch, q_heads, window);
-  return mq::attend_plan(a);
+  return mq::attend_plan(attend_args(cache, batch, q_heads, window), nullptr).bytes;
 }
 
 mq_status mq_cache_attend(const mq_kv_cache* cache, const mq_kv_batch* batch, const uint16_t* q,
@@ -204,7 +203,8 @@ mq_status mq_cache_attend(const mq_kv_cache* cache, const mq_kv_batch* batch, co
                                  out, lse);
   if (s != MQ_OK) return s;
   mq::AttendArgs a = attend_args(cache, batch, q_heads, window);
-  const size_t need = mq::attend_plan(a);
+  const mq::AttendPlan plan = mq::attend_plan(a, workspace);
+  const size_t need = plan.bytes;
   if (need > 0 && (!workspace || workspace_bytes < need)) return MQ_ERR_WORKSPACE;
   if (need > 0 && misaligned(workspace, 256)) return MQ_ERR_ALIGN;
   s = mq::device_check();
@@ -216,10 +216,7 @@ mq_status mq_cache_attend(const mq_kv_cache* cache, const mq_kv_batch* batch, co
   a.causal = causal;
   a.out = out;
   a.lse = lse;
-  a.part_o = static_cast<float*>(workspace);
-  if (need > 0)
-    a.part_ml = a.part_o + (size_t)a.pieces * a.batch.rows * a.q_heads * a.cache.dim;
-  return done(mq::launch_attend(a, (hipStream_t)stream));
+  return done(mq::launch_attend(a, plan, (hipStream_t)stream));
 }
 
 }  // extern "C"

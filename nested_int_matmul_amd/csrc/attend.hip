@@ -90,7 +90,7 @@ __device__ __forceinline__ Keys keys_of(const AttendArgs& a, int64_t pos, int he
 }
 
 // What the rows [row_a, row_b) of a (sequence, head) see together, as pieces
-// of a.piece tokens from a 64-aligned start.
+// of a.part.piece tokens from a 64-aligned start.
 struct Span {
   int lo, hi;  // lo a multiple of 64; lo >= hi: no key
   int pieces;
@@ -101,13 +101,20 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const SeqSpan& sp, 
   const Keys f = keys_of(a, sp.start + tok_a, held), l = keys_of(a, sp.start + tok_b, held);
   r.lo = f.lo & ~63;
   r.hi = l.hi;
-  r.pieces = r.hi > r.lo ? (r.hi - r.lo + a.piece - 1) / a.piece : 0;
+  r.pieces = r.hi > r.lo ? (r.hi - r.lo + a.part.piece - 1) / a.part.piece : 0;
   return r;
 }
 // row / group: rows are below 2^26 and groups at most 2^10, so a product with
 // ceil(2^36 / group) is off by less than 1 / group of a unit.
 __device__ __forceinline__ int token_of(const AttendArgs& a, int row) {
   return (int)(((uint64_t)(uint32_t)row * a.group_mul) >> 36);
+}
+// Where a row's partial results are within a piece's: few rows of a sequence
+// and head lie together (a batch may have many more rows than those), many
+// rows as in the output.
+__device__ __forceinline__ int64_t part_row(const AttendArgs& a, int s, int kvh, int row,
+                                            int64_t out_row) {
+  return a.part.tile <= 32 ? ((int64_t)s * a.cache.heads + kvh) * a.part.tile + row : out_row;
 }
 __device__ __forceinline__ int held_of(const AttendArgs& a, int s) {
   const int len = a.batch.kv_len[s];
@@ -139,8 +146,7 @@ __global__ void __launch_bounds__(NW * 64)
   __shared__ float lds_ml[NW][ROWS * 16][2];
 
   const int s = blockIdx.z;
-  const int kvh = blockIdx.x % a.cache.heads;
-  const int row_tile = blockIdx.x / a.cache.heads;
+  const int kvh = blockIdx.x;
   const int piece = blockIdx.y;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, r16 = lane & 15;
@@ -160,19 +166,17 @@ __global__ void __launch_bounds__(NW * 64)
     pk = ik < a.batch.table_pages ? table[ik] : -1;
     pv = iv < a.batch.table_pages ? table[iv] : -1;
   };
-  if (a.window == 0) pages(piece * a.piece + KT * wave);
+  if (a.window == 0) pages(piece * a.part.piece + KT * wave);
 
   const SeqSpan sp = seq_span(a.batch, s);
   const int rows = sp.n * a.group;  // rows of this sequence and head
-  const int row_base = row_tile * (ROWS * 16);
-  if (row_base >= rows) return;
-  const int row_last = row_base + ROWS * 16 < rows ? row_base + ROWS * 16 - 1 : rows - 1;
+  if (rows <= a.part.over || rows > a.part.upto) return;
   const int held = held_of(a, s);
-  const Span span = span_of(a, sp, held, token_of(a, row_base), token_of(a, row_last));
+  const Span span = span_of(a, sp, held, 0, token_of(a, rows - 1));
   if (piece > 0 && piece >= span.pieces) return;
 
-  const int begin = span.lo + piece * a.piece;
-  const int stop = begin + a.piece < span.hi ? begin + a.piece : span.hi;
+  const int begin = span.lo + piece * a.part.piece;
+  const int stop = begin + a.part.piece < span.hi ? begin + a.part.piece : span.hi;
   const int head_bytes = block * DIM;
   const int64_t page_bytes = (int64_t)head_bytes * a.cache.heads;
   const uint8_t* const kbase = a.cache.k + (int64_t)kvh * head_bytes + (r16 & 3) * DIM + 16 * g;
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(NW * 64)
   int see_lo[ROWS], see_hi[ROWS];
 #pragma unroll
   for (int rt = 0; rt < ROWS; ++rt) {
-    const int row = row_base + rt * 16 + r16;
+    const int row = rt * 16 + r16;
     const bool real = row < rows;
     const int tok = real ? token_of(a, row) : 0;
     const int head = kvh * a.group + (real ? row - tok * a.group : 0);
@@ -266,8 +270,8 @@ __global__ void __launch_bounds__(NW * 64)
     see_hi[rt] = real ? k.hi : 0;
   }
   // keys that every real row sees: no mask needed there
-  const Keys first = keys_of(a, sp.start + token_of(a, row_base), held);
-  const Keys last = keys_of(a, sp.start + token_of(a, row_last), held);
+  const Keys first = keys_of(a, sp.start, held);
+  const Keys last = keys_of(a, sp.start + token_of(a, rows - 1), held);
 
   f32x4 acc[ROWS][DT];
   float ref[ROWS], sum[ROWS];
@@ -446,7 +450,7 @@ __global__ void __launch_bounds__(NW * 64)
     // 16 rows x DIM outputs over NW * 64 threads, four at a time
     for (int i = threadIdx.x; i < 16 * (DIM / 4); i += NW * 64) {
       const int rr = i / (DIM / 4), d = (i % (DIM / 4)) * 4;
-      const int row = row_base + rt * 16 + rr;
+      const int row = rt * 16 + rr;
       if (row >= rows) continue;
       f32x4 o = *reinterpret_cast<f32x4*>(&lds_o[0][rr][d]);
 #pragma unroll
@@ -469,11 +473,11 @@ __global__ void __launch_bounds__(NW * 64)
         *reinterpret_cast<u32x2*>(a.out + out_row * DIM + d) = b;
         if (a.lse && d == 0) a.lse[out_row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
       } else {
-        const int64_t at = (int64_t)piece * a.batch.rows * a.q_heads + out_row;
-        *reinterpret_cast<f32x4*>(a.part_o + at * DIM + d) = o;
+        const int64_t at = piece * a.part.step + part_row(a, s, kvh, row, out_row);
+        *reinterpret_cast<f32x4*>(a.part.o + at * DIM + d) = o;
         if (d == 0) {
-          a.part_ml[2 * at] = mm;
-          a.part_ml[2 * at + 1] = ll;
+          a.part.ml[2 * at] = mm;
+          a.part.ml[2 * at + 1] = ll;
         }
       }
     }
@@ -524,6 +528,7 @@ __global__ void __launch_bounds__(NW * 64)
   const int kvh = blockIdx.x % a.cache.heads;
   const SeqSpan sp = seq_span(a.batch, s);
   const int rows = sp.n * a.group;
+  if (rows <= a.part.over || rows > a.part.upto) return;
   const int tiles = (rows + NW * 32 - 1) / (NW * 32);
   // last rows first: with a causal mask they see the most keys
   const int row_tile = tiles - 1 - (int)(blockIdx.x / a.cache.heads);
@@ -585,8 +590,8 @@ __global__ void __launch_bounds__(NW * 64)
   const Keys wf = keys_of(a, sp.start + (wreal ? token_of(a, wrow) : 0), held);
   const Keys wl = keys_of(a, sp.start + (wreal ? token_of(a, wlast) : 0), held);
 
-  const int begin = span.lo + piece * a.piece;
-  const int stop = begin + a.piece < span.hi ? begin + a.piece : span.hi;
+  const int begin = span.lo + piece * a.part.piece;
+  const int stop = begin + a.part.piece < span.hi ? begin + a.part.piece : span.hi;
   const int n_tiles = stop > begin ? (stop - begin + 63) >> 6 : 0;
   const int block = a.cache.block, shift = __builtin_ctz(block);
   const int head_bytes = block * DIM;
@@ -889,8 +894,8 @@ __global__ void __launch_bounds__(NW * 64)
       }
     if (a.lse && h == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
   } else {
-    const int64_t at = (int64_t)piece * a.batch.rows * a.q_heads + out_row;
-    float* o = a.part_o + at * DIM + 4 * h;
+    const int64_t at = piece * a.part.step + part_row(a, s, kvh, row, out_row);
+    float* o = a.part.o + at * DIM + 4 * h;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -898,97 +903,143 @@ __global__ void __launch_bounds__(NW * 64)
         *reinterpret_cast<f32x4*>(o + 32 * d + 8 * i) =
             f32x4{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
     if (h == 0) {
-      a.part_ml[2 * at] = ref;
-      a.part_ml[2 * at + 1] = sum;
+      a.part.ml[2 * at] = ref;
+      a.part.ml[2 * at + 1] = sum;
     }
   }
 }
 
 // ------------------------------------------------------------- the join
 //
-// One workgroup a row: 256 / (DIM / 4) groups of threads take the pieces in
-// turn, each with a reference, a sum and four outputs a thread of its own,
+// Threads of L = DIM / 4 a row hold four outputs each.
+//   Few rows have many pieces: a workgroup for each, whose 256 / L groups of
+// threads take the pieces in turn, each with a reference and a sum of its own,
 // joined through LDS.
+//   Many rows have few pieces: 256 / L rows a workgroup, each of which searches
+// for its sequence among the batch's.  (A workgroup a row, over a grid of the
+// longest prompt's rows for every sequence, took 1.1 ns a workgroup only to
+// start them: 8 prompts of 512 tokens 150 us.)
+//   One launch for both, whose first few_blocks workgroups are for few rows.
 template <int DIM>
-__global__ void __launch_bounds__(256) join_kernel(AttendArgs a, int tile_rows) {
-  constexpr int L = DIM / 4, G = 256 / L;
-  __shared__ f32x4 lds_o[G][L];
-  __shared__ float lds_ml[G][2];
-  const int s = blockIdx.z;
-  const int kvh = blockIdx.y;
-  const SeqSpan sp = seq_span(a.batch, s);
-  const int rows = sp.n * a.group;
-  const int row = blockIdx.x;
-  if (row >= rows) return;
-  const int held = held_of(a, s);
-  const int row_base = row / tile_rows * tile_rows;
-  const int row_last = row_base + tile_rows < rows ? row_base + tile_rows - 1 : rows - 1;
-  const Span span = span_of(a, sp, held, token_of(a, row_base), token_of(a, row_last));
-  if (span.pieces <= 1) return;  // written already
-  const int l = threadIdx.x % L, pg = threadIdx.x / L;
-  const int tok = token_of(a, row);
-  const int64_t out_row =
-      (int64_t)(sp.row0 + tok) * a.q_heads + kvh * a.group + (row - tok * a.group);
-  const int64_t step = a.batch.rows * a.q_heads;
+struct Joined {
   float m = kNoRef, sum = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int i0 = pg; i0 < span.pieces; i0 += 4 * G) {
+};
+template <int DIM>
+__device__ __forceinline__ void join_pieces(const AttendPart& p, int64_t first, int from, int by,
+                                            int pieces, int l, Joined<DIM>& r) {
+  for (int i0 = from; i0 < pieces; i0 += 4 * by) {
     float mi[4], si[4];
     f32x4 oi[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * G;
-      const int64_t at = out_row + (i < span.pieces ? i : i0) * step;
-      mi[j] = a.part_ml[2 * at];
-      si[j] = a.part_ml[2 * at + 1];
-      oi[j] = *reinterpret_cast<const f32x4*>(a.part_o + at * DIM + 4 * l);
+      const int i = i0 + j * by;
+      const int64_t at = first + (i < pieces ? i : i0) * p.step;
+      mi[j] = p.ml[2 * at];
+      si[j] = p.ml[2 * at + 1];
+      oi[j] = *reinterpret_cast<const f32x4*>(p.o + at * DIM + 4 * l);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (i0 + j * G >= span.pieces) continue;
-      const float top = fmaxf(m, mi[j]);
-      const float f = __builtin_amdgcn_exp2f(m - top), fi = __builtin_amdgcn_exp2f(mi[j] - top);
-      sum = sum * f + si[j] * fi;
-      o = o * f + oi[j] * fi;
-      m = top;
+      if (i0 + j * by >= pieces) continue;
+      const float top = fmaxf(r.m, mi[j]);
+      const float f = __builtin_amdgcn_exp2f(r.m - top), fi = __builtin_amdgcn_exp2f(mi[j] - top);
+      r.sum = r.sum * f + si[j] * fi;
+      r.o = r.o * f + oi[j] * fi;
+      r.m = top;
     }
   }
-  if (l == 0) {
-    lds_ml[pg][0] = m;
-    lds_ml[pg][1] = sum;
-  }
-  lds_o[pg][l] = o;
-  __syncthreads();
-  if (pg != 0) return;
-  float top = kNoRef;
-#pragma unroll
-  for (int i = 0; i < G; ++i) top = fmaxf(top, lds_ml[i][0]);
-  sum = 0.f;
-  o = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < G; ++i) {
-    const float f = __builtin_amdgcn_exp2f(lds_ml[i][0] - top);
-    sum += lds_ml[i][1] * f;
-    o = o + lds_o[i][l] * f;
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+}
+template <int DIM>
+__device__ __forceinline__ void put_joined(const AttendArgs& a, int64_t out_row, int l,
+                                           const Joined<DIM>& r) {
+  const float inv = r.sum == 0.f ? 0.f : 1.f / r.sum;
   u32x2 b;
-  b[0] = bf16_pair(o[0] * inv, o[1] * inv);
-  b[1] = bf16_pair(o[2] * inv, o[3] * inv);
-  if (sum == 0.f) b = u32x2{0, 0};
+  b[0] = bf16_pair(r.o[0] * inv, r.o[1] * inv);
+  b[1] = bf16_pair(r.o[2] * inv, r.o[3] * inv);
+  if (r.sum == 0.f) b = u32x2{0, 0};
   *reinterpret_cast<u32x2*>(a.out + out_row * DIM + 4 * l) = b;
-  if (a.lse && l == 0) a.lse[out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  if (a.lse && l == 0)
+    a.lse[out_row] = r.sum == 0.f ? -INFINITY : (r.m + log2f(r.sum)) * kLn2;
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(256)
+    join_kernel(AttendArgs a, AttendPlan plan, int few_rows, int few_blocks) {
+  constexpr int L = DIM / 4, G = 256 / L;
+  __shared__ f32x4 lds_o[G][L];
+  __shared__ float lds_ml[G][2];
+  const int kvh = blockIdx.y, bx = blockIdx.x;
+  const int l = threadIdx.x % L, pg = threadIdx.x / L;
+  const bool is_few = bx < few_blocks;
+  int s, row;
+  if (is_few) {
+    s = bx / few_rows;
+    row = bx - s * few_rows;
+  } else {
+    const int64_t all = (int64_t)(bx - few_blocks) * G + pg;
+    if (all >= a.batch.rows * a.group) return;
+    const int at = (int)((uint32_t)all / (uint32_t)a.group);
+    int end = a.batch.seqs;
+    for (s = 0; end - s > 1;) {
+      const int mid = (s + end) >> 1;
+      if (a.batch.q_start[mid] <= at)
+        s = mid;
+      else
+        end = mid;
+    }
+    row = (int)(all - (int64_t)seq_span(a.batch, s).row0 * a.group);
+  }
+  const SeqSpan sp = seq_span(a.batch, s);
+  const int rows = sp.n * a.group;
+  if (row < 0 || row >= rows) return;
+  a.part = plan.part[0];
+  for (int i = 1; i < plan.parts; ++i)
+    if (rows > plan.part[i].over) a.part = plan.part[i];
+  if (is_few != (a.part.tile <= 32)) return;
+  const int held = held_of(a, s);
+  const int tile = a.part.tile;
+  for (; row < rows; row += is_few ? few_rows : rows) {
+    const int row_base = row / tile * tile;
+    const int row_last = row_base + tile < rows ? row_base + tile - 1 : rows - 1;
+    const Span span = span_of(a, sp, held, token_of(a, row_base), token_of(a, row_last));
+    if (span.pieces <= 1) return;  // written already (a few rows' span is the same for all)
+    const int tok = token_of(a, row);
+    const int64_t out_row =
+        (int64_t)(sp.row0 + tok) * a.q_heads + kvh * a.group + (row - tok * a.group);
+    const int64_t first = part_row(a, s, kvh, row, out_row);
+    Joined<DIM> r;
+    if (!is_few) {
+      join_pieces<DIM>(a.part, first, 0, 1, span.pieces, l, r);
+      put_joined<DIM>(a, out_row, l, r);
+      return;
+    }
+    join_pieces<DIM>(a.part, first, pg, G, span.pieces, l, r);
+    if (l == 0) {
+      lds_ml[pg][0] = r.m;
+      lds_ml[pg][1] = r.sum;
+    }
+    lds_o[pg][l] = r.o;
+    __syncthreads();
+    if (pg == 0) {
+      r = Joined<DIM>();
+#pragma unroll
+      for (int i = 0; i < G; ++i) r.m = fmaxf(r.m, lds_ml[i][0]);
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const float f = __builtin_amdgcn_exp2f(lds_ml[i][0] - r.m);
+        r.sum += lds_ml[i][1] * f;
+        r.o = r.o + lds_o[i][l] * f;
+      }
+      put_joined<DIM>(a, out_row, l, r);
+    }
+    __syncthreads();
+  }
 }
 
 namespace {
 
-// Rows of a workgroup for max_new tokens of `group` heads each.
-// Up to 32 rows share the codes' way through one wave's registers; more are
-// worth converting the codes once for all of them.
 constexpr int many_waves(int dim) { return dim == 128 ? 8 : 4; }
-int rows_tile(int64_t most_rows, int dim) {
-  return most_rows <= 16 ? 16 : most_rows <= 32 ? 32 : many_waves(dim) * 32;
-}
 constexpr int kFewWaves = 4;
 
 // Keys of a wave's tile: 32 leave dim 256 two waves a SIMD (16 sequences of 8192 tokens:
@@ -1035,55 +1086,121 @@ hipError_t many(const AttendArgs& a, dim3 grid, hipStream_t s) {
 }
 
 template <int DIM>
-hipError_t attend_dim(AttendArgs& a, hipStream_t s) {
+hipError_t attend_part(AttendArgs& a, const AttendPart& part, hipStream_t s) {
+  a.part = part;
+  const int tile = part.tile;
   const int64_t most = (int64_t)a.batch.max_new * a.group;
-  const int tile = rows_tile(most, a.cache.dim);
-  const dim3 grid((unsigned)(a.cache.heads * ((most + tile - 1) / tile)), (unsigned)a.pieces,
+  const int64_t tiles = tile > 32 ? (most + tile - 1) / tile : 1;
+  const dim3 grid((unsigned)(a.cache.heads * tiles), (unsigned)part.pieces,
                   (unsigned)a.batch.seqs);
   constexpr int KT = few_keys(DIM);
-  hipError_t e = tile == 16   ? few<DIM, 1, kFewWaves, KT>(a, grid, s)
-                 : tile == 32 ? few<DIM, 2, kFewWaves, KT>(a, grid, s)
-                              : many<DIM>(a, grid, s);
-  if (e != hipSuccess || a.pieces <= 1) return e;
-  const dim3 jg((unsigned)most, (unsigned)a.cache.heads, (unsigned)a.batch.seqs);
-  hipLaunchKernelGGL((join_kernel<DIM>), jg, dim3(256), 0, s, a, tile);
+  return tile == 16   ? few<DIM, 1, kFewWaves, KT>(a, grid, s)
+         : tile == 32 ? few<DIM, 2, kFewWaves, KT>(a, grid, s)
+                      : many<DIM>(a, grid, s);
+}
+
+template <int DIM>
+hipError_t attend_dim(AttendArgs& a, const AttendPlan& plan, hipStream_t s) {
+  int64_t few_blocks = 0, many_blocks = 0;
+  constexpr int G = 256 / (DIM / 4);  // rows of a workgroup of the join
+  const int64_t most = (int64_t)a.batch.max_new * a.group;
+  // workgroups of the join for a sequence and head of few rows; beside prompts
+  // eight that take the rows in turn (32 that mostly find none cost 25 us for
+  // 200 sequences)
+  const int64_t few_rows = most <= 32 ? most : 8;
+  // (prompts first: they run longest)
+  for (int i = plan.parts - 1; i >= 0; --i) {
+    const AttendPart& p = plan.part[i];
+    const hipError_t e = attend_part<DIM>(a, p, s);
+    if (e != hipSuccess) return e;
+    if (p.pieces <= 1) continue;
+    if (p.tile <= 32)
+      few_blocks = few_rows * a.batch.seqs;
+    else
+      many_blocks = (a.batch.rows * a.group + G - 1) / G;
+  }
+  if (few_blocks + many_blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL((join_kernel<DIM>),
+                     dim3((unsigned)(few_blocks + many_blocks), (unsigned)a.cache.heads),
+                     dim3(256), 0, s, a, plan, (int)few_rows, (int)few_blocks);
   return hipGetLastError();
 }
 
-}  // namespace
-
-size_t attend_plan(AttendArgs& a) {
-  const int64_t most = (int64_t)a.batch.max_new * a.group;
-  const int tile = rows_tile(most, a.cache.dim);
+// Pieces of the longest span a row can see.  The lengths are not known here.
+//   Few rows: two workgroups a CU, counting every sequence.  With several of
+// them the longest possible span gets at least 16 pieces, so that long
+// sequences do not run on behind short ones (32 of up to 16384 tokens: 8
+// pieces 110 us, 16 103, 32 113).
+//   Many rows: one workgroup a CU, which is what fits of them at dim 128 (2048
+// tokens behind 2048, 32 heads of 128: one piece 146 us, two 222).  Counted are
+// the rows of the batch, not the longest prompt's for every sequence, by which
+// one prompt among single tokens would pass for 32 prompts and stay whole (512
+// tokens over 4096, seven single ones beside it: 106 us, by its rows 74).
+//   384 tokens a piece where that still fills the chip, 256 where it does not.
+void plan_part(const AttendArgs& a, int tile, int over, int upto, AttendPlan* plan) {
+  AttendPart* const p = &plan->part[plan->parts++];
+  p->tile = tile;
+  p->over = over;
+  p->upto = upto;
   int64_t keys = (int64_t)a.batch.table_pages * a.cache.block;
   if (a.window > 0 && a.window + a.batch.max_new + 64 < keys)
     keys = a.window + a.batch.max_new + 64;
-  const int64_t groups = (int64_t)a.batch.seqs * a.cache.heads * ((most + tile - 1) / tile);
-  // Two workgroups a CU; with several sequences, whose lengths the host does
-  // not know, at least 16 pieces of the longest possible one, so that long
-  // sequences do not run on behind short ones; and 384 tokens a piece where
-  // that still fills the chip, 256 where it does not.
-  int64_t pieces = (512 + groups - 1) / groups;
+  int64_t tiles = a.batch.seqs;
+  if (tile > 32) {
+    const int64_t most = (int64_t)a.batch.max_new * a.group, all = a.batch.rows * a.group;
+    tiles *= (most + tile - 1) / tile;
+    if (tiles > (all + tile - 1) / tile) tiles = (all + tile - 1) / tile;
+    if (tiles < 1) tiles = 1;
+  }
+  const int64_t groups = tiles * a.cache.heads;
+  const int64_t want = tile > 32 ? 256 : 512;
+  int64_t pieces = (want + groups - 1) / groups;
   if (tile <= 32 && a.batch.seqs > 1 && pieces < 16) pieces = 16;
   const int64_t least = groups * keys >= 512 * 256 ? 384 : 256;
   if (pieces > (keys + least - 1) / least) pieces = (keys + least - 1) / least;
   const int64_t grain = tile <= 32 ? few_keys(a.cache.dim) * kFewWaves : 64;
-  const int64_t piece = ((keys + pieces - 1) / pieces + grain - 1) / grain * grain;
-  a.piece = (int)piece;
-  a.pieces = (int)((keys + piece - 1) / piece);
-  if (a.pieces <= 1) {
-    a.pieces = 1;
-    return 0;
-  }
-  return (size_t)a.pieces * a.batch.rows * a.q_heads * (a.cache.dim + 2) * sizeof(float);
+  p->piece = (int)(((keys + pieces - 1) / pieces + grain - 1) / grain * grain);
+  p->pieces = (int)((keys + p->piece - 1) / p->piece);
+  p->step = tile <= 32 ? (int64_t)a.batch.seqs * a.cache.heads * tile : a.batch.rows * a.q_heads;
 }
 
-hipError_t launch_attend(AttendArgs& a, hipStream_t s) {
+}  // namespace
+
+// Up to 32 rows of a sequence and head share the codes' way through one wave's
+// registers; more are worth converting the codes once for all of them.  Where
+// prompts and steps come in one batch, each kind has a launch of its own: 512
+// tokens over 4096 with 31 single tokens over 8192 take 225 us (936 if all go
+// the prompts' way), with seven times six drafted tokens over 4096 81 us (168
+// if only up to 16 rows go the other way).  Two prompts of 64 tokens pay 1.5 of
+// 28 us for a launch that finds nothing.
+AttendPlan attend_plan(const AttendArgs& a, void* workspace) {
+  AttendPlan r{};
+  const int64_t most = (int64_t)a.batch.max_new * a.group;
+  const bool several = a.batch.seqs > 1;
+  if (most <= 32 || several) plan_part(a, most <= 16 ? 16 : 32, 0, 32, &r);
+  if (most > 32) plan_part(a, many_waves(a.cache.dim) * 32, several ? 32 : 0, 0x7fffffff, &r);
+  float* at = static_cast<float*>(workspace);
+  for (int i = 0; i < r.parts; ++i) {
+    AttendPart* const p = &r.part[i];
+    if (p->pieces <= 1) continue;
+    const size_t rows = (size_t)p->pieces * p->step;
+    // (each begins 16-byte aligned)
+    const size_t floats = (rows * (a.cache.dim + 2) + 3) & ~(size_t)3;
+    r.bytes += floats * sizeof(float);
+    if (!at) continue;
+    p->o = at;
+    p->ml = at + rows * a.cache.dim;
+    at += floats;
+  }
+  return r;
+}
+
+hipError_t launch_attend(AttendArgs& a, const AttendPlan& plan, hipStream_t s) {
   if (a.batch.rows == 0) return hipSuccess;
   switch (a.cache.dim) {
-    case 64: return attend_dim<64>(a, s);
-    case 128: return attend_dim<128>(a, s);
-    case 256: return attend_dim<256>(a, s);
+    case 64: return attend_dim<64>(a, plan, s);
+    case 128: return attend_dim<128>(a, plan, s);
+    case 256: return attend_dim<256>(a, plan, s);
     default: return hipErrorInvalidValue;
   }
 }

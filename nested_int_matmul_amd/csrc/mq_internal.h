@@ -150,6 +150,16 @@ struct RopeSpec {
   double factor;
   int rot, interleaved;
 };
+// One of the ways through the rows of a sequence and key/value head: the
+// sequences with over < rows <= upto, cut into pieces of `piece` tokens.
+struct AttendPart {
+  int tile;         // rows of a workgroup
+  int over, upto;
+  int piece, pieces;
+  int64_t step;     // rows of a piece's partial results
+  float* o;         // fp32 [pieces][step][dim]
+  float* ml;        // fp32 [pieces][step][2]
+};
 struct AttendArgs {
   KvCache cache;
   KvBatch batch;
@@ -162,10 +172,12 @@ struct AttendArgs {
   int causal;
   uint16_t* out;
   float* lse;
-  float* part_o;  // fp32 [pieces][rows][q_heads][dim]
-  float* part_ml; // fp32 [pieces][rows][q_heads][2]
-  int piece;      // tokens of one piece
-  int pieces;     // most pieces of a row (1: no workspace)
+  AttendPart part;  // of a launch
+};
+struct AttendPlan {
+  AttendPart part[2];
+  int parts;
+  size_t bytes;  // of all partial results
 };
 hipError_t launch_rope(const RopeSpec& r, const int* positions, const void* x, bool f32,
                        int64_t x_stride, int64_t rows, int heads, int dim, uint16_t* out,
@@ -176,9 +188,10 @@ hipError_t launch_cache_append(const KvCache& c, const KvBatch& b, const RopeSpe
                                hipStream_t s);
 hipError_t launch_cache_read(const KvCache& c, const KvBatch& b, void* k_out, void* v_out,
                              bool f32, hipStream_t s);
-// Bytes of partial results; fills piece and pieces.
-size_t attend_plan(AttendArgs& a);
-hipError_t launch_attend(AttendArgs& a, hipStream_t s);
+// Which rows go which way (a without its buffers); partial results from
+// `workspace` on.
+AttendPlan attend_plan(const AttendArgs& a, void* workspace);
+hipError_t launch_attend(AttendArgs& a, const AttendPlan& plan, hipStream_t s);
 // Argument checks of mq_cache_append and mq_cache_attend (device and workspace
 // left out), for calls made from inside the library.
 mq_status append_check(const mq_kv_cache* c, const mq_kv_batch* b, const mq_rope_spec* rope,

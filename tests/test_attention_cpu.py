@@ -210,6 +210,15 @@ def test_attend_refusals(L, kw, want):
     assert _attend(L, **kw) == want
 
 
+def test_attend_most_rows(L):
+    """Rows times query heads up to 2^25, the largest grid."""
+    c, most, more = _cache(), _batch(rows=1 << 20), _batch(rows=(1 << 20) + 1)
+    bytes_of = L.mq_cache_attend_workspace_bytes
+    assert bytes_of(ctypes.byref(c), ctypes.byref(most), 32, 0) > 0
+    assert bytes_of(ctypes.byref(c), ctypes.byref(more), 32, 0) == 0
+    assert _attend(L, b=more) == 2
+
+
 def test_attend_workspace(L):
     c, b = _cache(), _batch(seqs=2, rows=2, table_pages=512)
     need = L.mq_cache_attend_workspace_bytes(ctypes.byref(c), ctypes.byref(b), 32, 0)

@@ -358,6 +358,34 @@ def test_attend_pieces_of_ragged_batches():
     _attend_case(22, [2500, 3, 0, 700, 64], [9, 2, 0, 5, 7], 1, 4, 16, 64, "e4m3", window=600)
 
 
+@pytest.mark.parametrize("dim,fmt,group,softcap,window", [
+    (64, "int8", 4, 0.0, 0), (128, "e4m3", 4, 0.0, 0), (256, "int8", 2, 30.0, 0),
+    (128, "int8", 16, 0.0, 500), (128, "int8", 20, 0.0, 0)])
+def test_attend_prompts_and_steps_of_one_batch(dim, fmt, group, softcap, window):
+    """Chunks of prompts, drafted tokens, decode steps over short and long
+    sequences and idle slots together: each goes its own way, some in pieces."""
+    lens = [2500, 400, 1, 0, 1700, 65, 3000, 900]
+    new = [1, 400, 1, 0, 3, 65, 130, 1]
+    dev, batch, q, out = _attend_case(dim + group, lens, new, 2, group, 64, dim, fmt, softcap, window)
+    again = mq.cache_attend(dev, batch, device_bf16(q), scale=dim ** -0.5, softcap=softcap,
+                            window=window)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+
+
+def test_attend_prompts_among_many_sequences():
+    """More sequences than a wave has lanes: prompts first, last and between,
+    runs of idle slots, rows at the border of the two ways."""
+    rng = np.random.default_rng(5)
+    new = [1] * 150
+    for i, n in ((0, 40), (63, 33), (64, 32), (65, 70), (100, 150), (149, 90)):
+        new[i] = n
+    for i in (1, 2, 62, 66, 67, 128, 140):
+        new[i] = 0
+    lens = [int(n + rng.integers(0, 200)) for n in new]
+    _attend_case(6, lens, new, 2, 1, 32, 64, "int8")
+    _attend_case(7, lens[:90], new[:90], 1, 4, 32, 128, "e4m3")
+
+
 def test_attend_extreme_scores():
     """Scores of thousands and queries at the ends of bf16's range."""
     _attend_case(31, [150, 700], [2, 3], 2, 2, 32, 64, "int8", scale=3.0)
