@@ -11,18 +11,19 @@
 //   O^T [16 dims x 16 rows] += V^T [16 x 32 keys] P^T  (A = codes of v)
 // A row is one (token, query head of the group); a lane holds row lane % 16.
 // The order of the keys in a contraction is free as long as both operands
-// agree: MFMA t of a 64-key tile takes as its 16 rows the keys
-// 16 (r / 4) + 4 t + r % 4, which leaves lane group g = lane / 16 with the
-// scores of keys 16 g .. 16 g + 15: all of one page (a page is 16 tokens or
-// more, so one k scale and one v scale a lane), and the 16 consecutive bytes
-// that it loads of each dim of v.  No score and no code goes through LDS.
+// agree: with L = 16 (tiles of 64 keys) or 8 (of 32), MFMA t of a tile takes
+// as its 16 rows the keys L (r / 4) + 4 t + r % 4, which leaves lane group
+// g = lane / 16 with the scores of keys L g .. L g + L - 1: all of one page (a
+// page is 16 tokens or more, so one k scale and one v scale a lane), and the L
+// consecutive bytes that it loads of each dim of v.  No score and no code goes
+// through LDS.  (So for few rows; many rows share their codes through LDS.)
 //
 // Codes become fp16 exactly (int8 and e4m3 both fit), q becomes fp16 after
 // its row is multiplied by a power of two that brings its largest entry to
 // 2^14 (entries 2^-29 of that and above keep all their bits), the products
 // accumulate in fp32.  Probabilities are rounded to fp16, in units of a
-// reference that stays within 2^8 of the row's maximum: their error is
-// 2^-12 relative, below that of the bf16 result.
+// reference that stays within 2^8 of the row's maximum: off by at most
+// 2^-11 of each, an eighth of the result's own rounding to bf16 (2^-8).
 #include "kv_device.h"
 
 namespace mq {
@@ -127,12 +128,16 @@ __device__ __forceinline__ int held_of(const AttendArgs& a, int s) {
 // ------------------------------------------------------------- few rows
 //
 // ROWS * 16 rows a workgroup, NW waves that share them and take the piece's
-// 64-key tiles in turn, each with sums of its own, joined through LDS at the
-// end; pieces are joined by join_kernel.  Bound by the codes' bytes.
-// Waves of a SIMD that the registers are cut for (k and v of a tile, the
-// outputs, the queries).
+// tiles in turn, each with sums of its own, joined through LDS at the end;
+// pieces are joined by join_kernel.  Bound by the codes' bytes: 464 MB of 32
+// sequences in 103 us with the join (4.5 TB/s, nearly the rate of a large
+// copy), one sequence of 131072 tokens (268 MB) in 56 us.  Short spans are
+// bound by the way of a piece: lengths, table, codes, two products, the join
+// (one token over 700: 7 us, and 3 for the join).
+//   few_waves: waves of a SIMD that the registers are cut for (k and v of a
+// tile, the outputs, the queries).
 constexpr int few_waves(int dim, int rows, int kt) {
-  return  dim * (rows + kt / 32) <= 256 ? 3 : dim * (rows + kt / 32) <= 512 ? 2 : 1;
+  return dim * (rows + kt / 32) <= 256 ? 3 : dim * (rows + kt / 32) <= 512 ? 2 : 1;
 }
 
 template <int DIM, int ROWS, int KT, int NW, bool E4M3, bool CAP>
@@ -497,6 +502,8 @@ __global__ void __launch_bounds__(NW * 64)
 // of the tile in registers 8 e .. 8 e + 7: eight consecutive keys of one
 // 16-key group, the operand of the second product as it stands.  A 16-key
 // group lies in one page, so its scales are the same for all lanes.
+// Two prompts of up to 2048 tokens behind up to 6144 (32 heads of 128 over 8):
+// 430 us, 870 TFLOP/s; unstaged, with 64 rows a workgroup, 976.
 //
 // What bounds it is the vector unit beside the matrix unit: an exp2 (four
 // issue slots), a multiply-add, an addition, half a maximum and half a

@@ -13,7 +13,8 @@ constexpr int kThreads = 256;
 // over `per` heads, four at a time in flight, so the four float64 sines and
 // cosines (about 45 instructions a pair) are found once for all of them; the
 // angles do not depend on the head.  Lanes of a wave hold consecutive units:
-// 8 or 16 bytes each, whole lines together.
+// 8 or 16 bytes each, whole lines together.  8192 tokens of 32 x 128 bf16 (134
+// MB in and out): 26 us, 5.1 TB/s, the rate of a large copy.
 template <bool F32>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeSpec r, const int* positions,
                                                         const void* x, int64_t x_stride,
@@ -84,6 +85,10 @@ hipError_t launch_rope(const RopeSpec& r, const int* positions, const void* x, b
 // v is held dim-major: pages that get 16 tokens or more go through LDS, four
 // tokens of a dim to a dword, and leave in 16-byte pieces; fewer tokens go out
 // as single bytes.
+// 8192 tokens of 8 x 256 with 16 heads of queries turned (235 MB): 67 us from
+// HBM, 56 where the activations are still in the last-level cache (3.5 and 4.2
+// TB/s); the turns, in float64, take 9 of them.  A step of 32 tokens: 5 us, a
+// chain of dependent loads (lengths, table, scale) and two barriers.
 //
 // The queries' workgroups (blockIdx.y >= 2 * heads) take eight tokens of the
 // same page each, all heads.
@@ -452,8 +457,9 @@ hipError_t launch_cache_append(const KvCache& c, const KvBatch& b, const RopeSpe
 
 // ----------------------------------------------------------- mq_cache_read
 //
-// One workgroup per (sequence, page, head, k or v).  Four codes a load; v is
-// turned from dim-major through LDS.
+// One workgroup per (sequence, page, head, k or v).  Eight codes of k and 16
+// of v a load; v is turned from dim-major through LDS.  Four sequences of up to
+// 16384 tokens, 8 x 128 to bf16 (286 MB): 51 us on the GPU, 5.6 TB/s.
 template <int DIM, int BLOCK>
 __global__ void __launch_bounds__(kThreads) read_kernel(KvCache cache, KvBatch b, void* k_out,
                                                         void* v_out, bool f32) {
