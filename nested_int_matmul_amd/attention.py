@@ -132,6 +132,15 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _output(t, name, dtype, device, shape, stream):
+    """The tensor that the call writes and its address: the given one, checked,
+    or a new one."""
+    if t is None:
+        t = _empty(shape, dtype, device, stream)
+        return t, t.data_ptr()
+    return t, _address(t, name, (dtype,), device, shape)
+
+
 def _rows_view(x, name, device, heads=None, dim=None, rows=None):
     """x bf16 or fp32 [rows, heads, dim] on `device` whose rows are contiguous
     and evenly spaced (it may be a part of wider rows): (type, row stride in
@@ -387,9 +396,7 @@ def _append_call(cache, batch, k, v, q, rope, q_out, stream):
             raise TypeError("mq: q has another type than k and v")
         shape = tuple(q.shape)
         q_heads = shape[1]
-        if q_out is None:
-            q_out = _empty(shape, torch.bfloat16, dev, stream)
-        po = _address(q_out, "q_out", (torch.bfloat16,), dev, shape)
+        q_out, po = _output(q_out, "q_out", torch.bfloat16, dev, shape, stream)
     elif q_out is not None:
         raise ValueError("mq: q_out without q")
     return (cache.ref, batch.ref, rope.ref if rope is not None else None, pk, pv, stride, pq,
@@ -430,13 +437,9 @@ def cache_read(cache: KVCache, batch: KVBatch, dtype=None, k_out=None, v_out=Non
     dev = cache.device
     _one_device(dev, batch)
     shape = (batch.rows, cache.heads, cache.dim)
-    if k_out is None:
-        k_out = _empty(shape, dtype, dev, stream)
-    if v_out is None:
-        v_out = _empty(shape, dtype, dev, stream)
-    args = (cache.ref, batch.ref, _address(k_out, "k_out", (dtype,), dev, shape),
-            _address(v_out, "v_out", (dtype,), dev, shape),
-            _F32 if dtype is torch.float32 else _BF16, at)
+    k_out, pk = _output(k_out, "k_out", dtype, dev, shape, stream)
+    v_out, pv = _output(v_out, "v_out", dtype, dev, shape, stream)
+    args = (cache.ref, batch.ref, pk, pv, _F32 if dtype is torch.float32 else _BF16, at)
     _run(lib().mq_cache_read, "mq_cache_read", args, batch.rows)
     return k_out, v_out
 
@@ -456,17 +459,16 @@ def _attend_call(cache, batch, q, scale, softcap, window, causal, out, lse, work
         raise TypeError("mq: q must be bf16")
     _one_device(dev, cache, batch)
     t, h, d = q.shape
-    if out is None:
-        out = _empty((t, h, d), torch.bfloat16, dev, stream)
-    po = _address(out, "out", (torch.bfloat16,), dev, (t, h, d))
+    out, po = _output(out, "out", torch.bfloat16, dev, (t, h, d), stream)
     pl = None if lse is None else _address(lse, "lse", (torch.float32,), dev, (t, h))
-    if workspace is None:
-        need = cache_attend_workspace_bytes(cache, batch, h, window)
-        if need:
-            workspace = _empty((need,), torch.uint8, dev, stream)
     pw, nw = None, 0
     if workspace is not None:
         pw, nw = _address(workspace, "workspace", (torch.uint8,), dev), workspace.numel()
+    else:
+        nw = cache_attend_workspace_bytes(cache, batch, h, window)
+        if nw:
+            workspace = _empty((nw,), torch.uint8, dev, stream)
+            pw = workspace.data_ptr()
     return (cache.ref, batch.ref, pq, stride, h, d ** -0.5 if scale is None else scale, softcap,
             window, 1 if causal else 0, po, pl, pw, nw, at), t, out, workspace
 
@@ -544,9 +546,7 @@ def mixnmatch_attend(layer_arr, attn: StackAttention, x=None, h=None, workspace=
     px = None
     if x is not None:
         px = _address(x, "x", (torch.bfloat16, torch.int16, torch.uint16), dev, (m, H))
-    if h is None:
-        h = _empty((m, H), torch.float32, dev, stream)
-    ph = _address(h, "h", (torch.float32,), dev, (m, H))
+    h, ph = _output(h, "h", torch.float32, dev, (m, H), stream)
     if workspace is None:
         need = mixnmatch_attend_workspace_bytes(layer_arr, attn, m)
         workspace = _empty((max(need, 1),), torch.uint8, dev, stream)
