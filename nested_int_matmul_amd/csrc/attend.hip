@@ -117,6 +117,17 @@ __device__ __forceinline__ int64_t part_row(const AttendArgs& a, int s, int kvh,
                                             int64_t out_row) {
   return a.part.tile <= 32 ? ((int64_t)s * a.cache.heads + kvh) * a.part.tile + row : out_row;
 }
+// (blockIdx.y + blockIdx.z) % pieces.  Workgroups are dealt to the parts of the
+// chip in turn, those that find nothing too: were every sequence's first piece
+// the first of a multiple of four, one part would get the pieces that all
+// sequences have and another those that few have (32 sequences of up to 16384
+// tokens in 16 pieces each: 102.3 us, turned 99.6; with the pieces outermost
+// 127).
+__device__ __forceinline__ int turned_piece(const AttendPart& p) {
+  const uint32_t z = blockIdx.z;
+  const int i = (int)(blockIdx.y + (z - p.pieces * (uint32_t)(((uint64_t)z * p.turn) >> 31)));
+  return i < p.pieces ? i : i - p.pieces;
+}
 __device__ __forceinline__ int held_of(const AttendArgs& a, int s) {
   const int len = a.batch.kv_len[s];
   const int room = a.batch.table_pages * a.cache.block;
@@ -130,7 +141,7 @@ __device__ __forceinline__ int held_of(const AttendArgs& a, int s) {
 // ROWS * 16 rows a workgroup, NW waves that share them and take the piece's
 // tiles in turn, each with sums of its own, joined through LDS at the end;
 // pieces are joined by join_kernel.  Bound by the codes' bytes: 464 MB of 32
-// sequences in 103 us with the join (4.5 TB/s, nearly the rate of a large
+// sequences in 96 us with the join (4.8 TB/s, nearly the rate of a large
 // copy), one sequence of 131072 tokens (268 MB) in 56 us.  Short spans are
 // bound by the way of a piece: lengths, table, codes, two products, the join
 // (one token over 700: 7 us, and 3 for the join).
@@ -152,7 +163,7 @@ __global__ void __launch_bounds__(NW * 64)
 
   const int s = blockIdx.z;
   const int kvh = blockIdx.x;
-  const int piece = blockIdx.y;
+  const int piece = turned_piece(a.part);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, r16 = lane & 15;
 
@@ -1134,10 +1145,15 @@ hipError_t attend_dim(AttendArgs& a, const AttendPlan& plan, hipStream_t s) {
 }
 
 // Pieces of the longest span a row can see.  The lengths are not known here.
-//   Few rows: two workgroups a CU, counting every sequence.  With several of
-// them the longest possible span gets at least 16 pieces, so that long
-// sequences do not run on behind short ones (32 of up to 16384 tokens: 8
-// pieces 110 us, 16 103, 32 113).
+//   Few rows: two workgroups a CU, counting every sequence.  With several
+// sequences more pieces keep the long ones from running on behind the short
+// ones, but each has a start and a join, which cost about as much as 256
+// tokens.  A place on the chip with W = groups * keys / 512 tokens to read
+// takes W (1 + 256 / piece) + piece / 2: least at piece^2 = 512 W, which is
+// (keys / piece)^2 = keys / groups; taken to the next power of two (others
+// fall unevenly on the chip).  32 sequences of up to 16384 tokens: 4 pieces
+// 112 us, 8 (this rule) 95.8, 12 99.7, 16 99.6; 128 of 8192: 4 (this rule)
+// 397, 16 452.
 //   Many rows: one workgroup a CU, which is what fits of them at dim 128 (2048
 // tokens behind 2048, 32 heads of 128: one piece 146 us, two 222).  Counted are
 // the rows of the batch, not the longest prompt's for every sequence, by which
@@ -1162,12 +1178,17 @@ void plan_part(const AttendArgs& a, int tile, int over, int upto, AttendPlan* pl
   const int64_t groups = tiles * a.cache.heads;
   const int64_t want = tile > 32 ? 256 : 512;
   int64_t pieces = (want + groups - 1) / groups;
-  if (tile <= 32 && a.batch.seqs > 1 && pieces < 16) pieces = 16;
+  if (tile <= 32 && a.batch.seqs > 1) {
+    int64_t split = 1;
+    while (split * split * groups < keys) split *= 2;
+    if (pieces < split) pieces = split;
+  }
   const int64_t least = groups * keys >= 512 * 256 ? 384 : 256;
   if (pieces > (keys + least - 1) / least) pieces = (keys + least - 1) / least;
   const int64_t grain = tile <= 32 ? few_keys(a.cache.dim) * kFewWaves : 64;
   p->piece = (int)(((keys + pieces - 1) / pieces + grain - 1) / grain * grain);
   p->pieces = (int)((keys + p->piece - 1) / p->piece);
+  p->turn = (uint32_t)((((uint64_t)1 << 31) + p->pieces - 1) / p->pieces);
   p->step = tile <= 32 ? (int64_t)a.batch.seqs * a.cache.heads * tile : a.batch.rows * a.q_heads;
 }
 
@@ -1176,7 +1197,7 @@ void plan_part(const AttendArgs& a, int tile, int over, int upto, AttendPlan* pl
 // Up to 32 rows of a sequence and head share the codes' way through one wave's
 // registers; more are worth converting the codes once for all of them.  Where
 // prompts and steps come in one batch, each kind has a launch of its own: 512
-// tokens over 4096 with 31 single tokens over 8192 take 225 us (936 if all go
+// tokens over 4096 with 31 single tokens over 8192 take 212 us (936 if all go
 // the prompts' way), with seven times six drafted tokens over 4096 81 us (168
 // if only up to 16 rows go the other way).  Two prompts of 64 tokens pay 1.5 of
 // 28 us for a launch that finds nothing.

@@ -156,6 +156,7 @@ struct AttendPart {
   int tile;         // rows of a workgroup
   int over, upto;
   int piece, pieces;
+  uint32_t turn;    // ceil(2^31 / pieces)
   int64_t step;     // rows of a piece's partial results
   float* o;         // fp32 [pieces][step][dim]
   float* ml;        // fp32 [pieces][step][2]
