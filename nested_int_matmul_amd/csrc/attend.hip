@@ -1159,7 +1159,11 @@ hipError_t attend_dim(AttendArgs& a, const AttendPlan& plan, hipStream_t s) {
 // the rows of the batch, not the longest prompt's for every sequence, by which
 // one prompt among single tokens would pass for 32 prompts and stay whole (512
 // tokens over 4096, seven single ones beside it: 106 us, by its rows 74).
-//   384 tokens a piece where that still fills the chip, 256 where it does not.
+//   384 tokens a piece where that still fills the chip, 256 where it does not;
+// and few rows of a short span are not cut at all, since the join costs as much
+// as two or three turns of a workgroup and more where there are many (one token
+// over 500: 8.7 us against 10.3, over 1000 12.4 against 10.5; 16 over 700 10.7
+// against 13.2, over 1000 14.1 against 13.5; 64 over 1000 24.0 against 32.9).
 void plan_part(const AttendArgs& a, int tile, int over, int upto, AttendPlan* plan) {
   AttendPart* const p = &plan->part[plan->parts++];
   p->tile = tile;
@@ -1176,6 +1180,7 @@ void plan_part(const AttendArgs& a, int tile, int over, int upto, AttendPlan* pl
     if (tiles < 1) tiles = 1;
   }
   const int64_t groups = tiles * a.cache.heads;
+  const int64_t step = few_keys(a.cache.dim) * kFewWaves;  // few rows: keys of a workgroup's turn
   const int64_t want = tile > 32 ? 256 : 512;
   int64_t pieces = (want + groups - 1) / groups;
   if (tile <= 32 && a.batch.seqs > 1) {
@@ -1185,7 +1190,9 @@ void plan_part(const AttendArgs& a, int tile, int over, int upto, AttendPlan* pl
   }
   const int64_t least = groups * keys >= 512 * 256 ? 384 : 256;
   if (pieces > (keys + least - 1) / least) pieces = (keys + least - 1) / least;
-  const int64_t grain = tile <= 32 ? few_keys(a.cache.dim) * kFewWaves : 64;
+  const int64_t half_turns = groups >= 256 ? 8 : groups >= 64 ? 6 : 5;
+  if (tile <= 32 && 2 * keys <= half_turns * step) pieces = 1;
+  const int64_t grain = tile <= 32 ? step : 64;
   p->piece = (int)(((keys + pieces - 1) / pieces + grain - 1) / grain * grain);
   p->pieces = (int)((keys + p->piece - 1) / p->piece);
   p->turn = (uint32_t)((((uint64_t)1 << 31) + p->pieces - 1) / p->pieces);

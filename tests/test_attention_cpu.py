@@ -212,7 +212,8 @@ def test_attend_refusals(L, kw, want):
 
 def test_attend_most_rows(L):
     """Rows times query heads up to 2^25, the largest grid."""
-    c, most, more = _cache(), _batch(rows=1 << 20), _batch(rows=(1 << 20) + 1)
+    c = _cache()
+    most, more = (_batch(rows=n, table_pages=512) for n in (1 << 20, (1 << 20) + 1))
     bytes_of = L.mq_cache_attend_workspace_bytes
     assert bytes_of(ctypes.byref(c), ctypes.byref(most), 32, 0) > 0
     assert bytes_of(ctypes.byref(c), ctypes.byref(more), 32, 0) == 0
